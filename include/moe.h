@@ -503,6 +503,92 @@ int moe_backward(const void* dout, const void* x, const void* w_router, const mo
                  void* dx, float* dw_router, float* dbias, void* dw_gate_up, void* dw_down,
                  void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------- */
+/* Operators around the layer: what turns tokens into its input rows, what adds  */
+/* its output to the residual stream, and what reads the logits at the end, each */
+/* with its gradient.                                                            */
+/*   - Matrices are rows of MOE_F32 or MOE_BF16 elements, `ld` elements apart    */
+/*     (ld >= columns), at any element alignment.  Rows in whole 16-byte aligned */
+/*     groups of eight elements move fastest.                                    */
+/*   - Token ids are int32 or int64 (id_bytes 4 or 8).                           */
+/*   - `workspace` is needed for its status header only (256 bytes, zeroed with  */
+/*     moe_workspace_init), except where a size is given; NULL: device errors    */
+/*     are not reported.                                                         */
+/*   - All sums are FP32, and each result is rounded once.  No entry point uses  */
+/*     atomics on values: the same inputs give the same bits.                    */
+/* ------------------------------------------------------------------------- */
+
+/* Token embedding:  out[n] = scale * table[ids[n]].
+ *   ids : [N];  table : [V][H] (table_dtype);  out : [N][H] (out_dtype)
+ * A negative id is "no token" and gives a zero row.  An id of V or more does too and
+ * records MOE_ERR_DEVICE_CHECK.  N <= 2^30, V < 2^31, H <= 2^24. */
+int moe_embedding(const void* ids, int id_bytes, int64_t N, const void* table, int table_dtype,
+                  int64_t V, int64_t H, int64_t ld_table, float scale, void* out, int out_dtype,
+                  int64_t ld_out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of the embedding table, by tokens sorted by id:
+ *   dtable[v] = scale * sum over n with ids[n] = v of dout[n]   (+ dtable[v], accumulate)
+ * summed in token order in FP32 (ranges of 32 sorted tokens, then the ranges in order).
+ * Without `accumulate` every row of dtable is written, zeros where no token names it;
+ * with it only the rows that tokens name are touched.  Negative ids take no part; an id
+ * of V or more takes none and records MOE_ERR_DEVICE_CHECK.
+ *   dout : [N][H] (dout_dtype);  dtable : [V][H] (dtable_dtype)             (out)
+ *   workspace : moe_embedding_workspace_bytes(N, V, H) bytes (0 for an invalid shape) */
+size_t moe_embedding_workspace_bytes(int64_t N, int64_t V, int64_t H);
+int moe_embedding_backward(const void* ids, int id_bytes, int64_t N, int64_t V, int64_t H,
+                           const void* dout, int dout_dtype, int64_t ld_dout, float scale,
+                           void* dtable, int dtable_dtype, int64_t ld_dtable, int accumulate,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Log probabilities of given tokens, entropy, and the most likely alternatives, of the
+ * distributions softmax(scale * logits[r]) (scale = 1 / temperature, positive):
+ *   logits   : [T][V] (dtype), V <= 2^22
+ *   targets  : [T] token ids, or NULL; a negative target is "none": its logp is 0.  One
+ *              of V or more is too and records MOE_ERR_DEVICE_CHECK
+ *   logp     : [T] FP32 log probability of the target (NULL exactly with targets) (out)
+ *   entropy  : [T] FP32, in nats, or NULL                                   (out)
+ *   stats    : [T][2] FP32 row maximum m and ln sum exp(scale (x - m)), which the
+ *              gradient reads, or NULL                                      (out)
+ *   top_idx, top_logp : [T][n_top] int32 / FP32, the n_top (0..32, <= V) largest
+ *              logits of each row in descending order, equal logits by ascending
+ *              index (-0 equals +0), and their log probabilities            (out)
+ * A logit of -inf is masked out.  A row that is masked throughout gives logp -inf (also
+ * in its top list, the lowest indices), entropy 0.  A row with a NaN or +inf gives NaN,
+ * and its top list is some list of valid indices. */
+int moe_token_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld, float scale,
+                       const void* targets, int id_bytes, float* logp, float* entropy, float* stats,
+                       int n_top, int32_t* top_idx, float* top_logp, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* Gradient of moe_token_logprobs with respect to the logits, for the gradients g_logp and
+ * g_entropy of its two outputs (either may be NULL, not both):
+ *   dlogits[r][j] = scale * ( g_logp (1[j = target] - p_j)
+ *                             - g_entropy * p_j * (logp_j + entropy) )
+ *   stats, entropy : moe_token_logprobs's (entropy only with g_entropy)
+ *   dlogits : [T][V] (dtype); may be the logits themselves (with ld_dlogits = ld) (out)
+ * Masked logits and rows that are masked throughout get 0; a row without a target gets
+ * the entropy's part only. */
+int moe_token_logprobs_backward(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
+                                float scale, const void* targets, int id_bytes, const float* stats,
+                                const float* entropy, const float* g_logp, const float* g_entropy,
+                                void* dlogits, int64_t ld_dlogits, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* Dropout with the residual add; the mask is a function of (seed, offset, row, column) and
+ * is never stored:
+ *   out[r][c] = residual[r][c] + (bits(r, c) >= thr ? x[r][c] * 65536 / (65536 - thr) : 0)
+ *   thr = round(65536 p), 0 <= p <= 1 (thr = 65536 drops everything)
+ *   bits(r, c) : the 16 bits number c % 8 (low half of the first word first) of
+ *                Philox4x32-10 with key (seed low, seed high) and counter (b low, b high,
+ *                offset low, offset high), b = r * ceil(cols / 8) + c / 8
+ *   x, residual (or NULL: 0), out : [rows][cols] (dtype); out may be x or residual itself
+ *                (with the same ld)
+ * A dropped element of x does not reach the result, whatever it holds.  The gradient with
+ * respect to x is the same call on the gradient of out, without a residual. */
+int moe_dropout(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                const void* residual, int64_t ld_residual, double p, uint64_t seed, uint64_t offset,
+                void* out, int64_t ld_out, void* stream);
+
 /* Smallest minibatch (in slots) that gives `waves` full waves of GEMM1 tiles of
  * tile_m x tile_n over `compute_sms` SMs when GEMM1 has 2*I output columns
  * ([MoK-2.37x] section 02: a minibatch should form at least two full waves; the

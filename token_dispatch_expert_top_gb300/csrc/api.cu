@@ -2,11 +2,13 @@
 // checks, the workspace plan, and the launch sequences.  No function here
 // allocates device memory or synchronises the host (except
 // moe_last_device_status, whose job is to).
+#include <math.h>
 #include <stdio.h>
 #include <string.h>
 
 #include "common.cuh"
 #include "kernels.cuh"
+#include "vec_io.cuh"
 
 namespace moe {
 namespace {
@@ -256,6 +258,61 @@ int expert_ffn_impl(const void* a, const void* a_scales, int a_rows, const int32
     c.timeout_ns = timeout;
     c.grid = num_sms_current();
     return cuda_status(launch_expert_ffn_tc(c, st));
+}
+
+// ---- operators around the layer (embedding, token log probabilities, dropout)
+
+// Rows of `cols` FP32 or BF16 elements, `ld` elements apart.
+bool rows_ok(const void* p, int dtype, int64_t rows, int64_t cols, int64_t ld) {
+    if (dtype != MOE_F32 && dtype != MOE_BF16) return false;
+    if (ld < cols || (rows > 0 && ld > (1ll << 60) / rows)) return false;
+    return p && (uintptr_t)p % dtype_bytes(dtype) == 0;
+}
+
+bool ids_ok(const void* p, int id_bytes) {
+    return (id_bytes == 4 || id_bytes == 8) && p && (uintptr_t)p % id_bytes == 0;
+}
+
+bool finite_positive(float v) { return v > 0.f && v <= 3.4028234e38f; }
+
+// A workspace that only has to hold the status header; none: nothing is reported.
+int check_status_ws(void* ws, size_t bytes) {
+    if (!ws) return MOE_OK;
+    return ((uintptr_t)ws & 31) || bytes < sizeof(WsHeader) ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
+// Workspace regions of moe_embedding_backward, in order.
+struct EmbedPlan {
+    size_t n_live, order, key, part, total;
+};
+
+EmbedPlan make_embed_plan(int64_t N, int64_t H) {
+    EmbedPlan pl{};
+    size_t off = align256(sizeof(WsHeader));
+    auto take = [&](size_t bytes) {
+        size_t o = off;
+        off += align256(bytes);
+        return o;
+    };
+    pl.n_live = take(sizeof(int32_t));
+    pl.order = take(sizeof(int32_t) * (size_t)N);
+    pl.key = take(sizeof(int32_t) * (size_t)N);
+    pl.part = take(sizeof(float) * 2 * (size_t)embed_ranges(N) * (size_t)((H + 7) / 8 * 8));
+    pl.total = off;
+    return pl;
+}
+
+int check_embed_shape(int64_t N, int64_t V, int64_t H) {
+    if (N < 0 || V <= 0 || H <= 0) return MOE_ERR_INVALID_ARG;
+    if (N > (1 << 30) || V > 0x7fffffffLL || H > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+int check_logits(int dtype, int64_t T, int64_t V, float scale) {
+    if (T < 0 || V <= 0 || !finite_positive(scale)) return MOE_ERR_INVALID_ARG;
+    if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+    if (T > 0x7fffffffLL || V > kMaxLogprobVocab) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
 }
 
 }  // namespace
@@ -994,6 +1051,150 @@ int moe_backward(const void* dout, const void* x, const void* w_router, const mo
     return moe_expert_wgrad(at<void>(ws, pl.duv), x, dout, saved->uv, saved->sched,
                             at<float>(ws, pl.slot_gate), saved->offsets, shape, dw_gate_up, dw_down,
                             ws, workspace_bytes, stream);
+}
+
+// ------------------------------------------------- operators around the layer
+int moe_embedding(const void* ids, int id_bytes, int64_t N, const void* table, int table_dtype, int64_t V, int64_t H,
+                  int64_t ld_table, float scale, void* out, int out_dtype, int64_t ld_out, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+    int rc = check_embed_shape(N, V, H);
+    if (rc) return rc;
+    if (!(scale >= -3.4028234e38f && scale <= 3.4028234e38f)) return MOE_ERR_INVALID_ARG;
+    if (id_bytes != 4 && id_bytes != 8) return MOE_ERR_INVALID_ARG;
+    if (N == 0) return MOE_OK;
+    if (!ids_ok(ids, id_bytes) || !rows_ok(table, table_dtype, V, H, ld_table) ||
+        !rows_ok(out, out_dtype, N, H, ld_out))
+        return MOE_ERR_INVALID_ARG;
+    rc = check_status_ws(workspace, workspace_bytes);
+    if (rc) return rc;
+    return cuda_status(launch_embedding(ids, id_bytes, N, table, table_dtype, V, H, ld_table, scale, out, out_dtype,
+                                        ld_out, num_sms_current(), (WsHeader*)workspace, (cudaStream_t)stream));
+}
+
+size_t moe_embedding_workspace_bytes(int64_t N, int64_t V, int64_t H) {
+    if (check_embed_shape(N, V, H) != MOE_OK) return 0;
+    return make_embed_plan(N, H).total;
+}
+
+int moe_embedding_backward(const void* ids, int id_bytes, int64_t N, int64_t V, int64_t H, const void* dout,
+                           int dout_dtype, int64_t ld_dout, float scale, void* dtable, int dtable_dtype,
+                           int64_t ld_dtable, int accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_embed_shape(N, V, H);
+    if (rc) return rc;
+    if (!(scale >= -3.4028234e38f && scale <= 3.4028234e38f)) return MOE_ERR_INVALID_ARG;
+    if (id_bytes != 4 && id_bytes != 8) return MOE_ERR_INVALID_ARG;
+    if (!rows_ok(dtable, dtable_dtype, V, H, ld_dtable)) return MOE_ERR_INVALID_ARG;
+    if (N == 0 && accumulate) return MOE_OK;
+    if (N > 0 && (!ids_ok(ids, id_bytes) || !rows_ok(dout, dout_dtype, N, H, ld_dout))) return MOE_ERR_INVALID_ARG;
+    const EmbedPlan pl = make_embed_plan(N, H);
+    if (!workspace || ((uintptr_t)workspace & 31) || workspace_bytes < pl.total) return MOE_ERR_WORKSPACE;
+    EmbedBackward c{};
+    c.ids = ids;
+    c.id_bytes = id_bytes;
+    c.N = N;
+    c.V = V;
+    c.H = H;
+    c.dout = dout;
+    c.dout_dtype = dout_dtype;
+    c.ld_dout = ld_dout;
+    c.scale = scale;
+    c.dtable = dtable;
+    c.dtable_dtype = dtable_dtype;
+    c.ld_dtable = ld_dtable;
+    c.accumulate = accumulate != 0;
+    c.order = at<int32_t>(workspace, pl.order);
+    c.key = at<int32_t>(workspace, pl.key);
+    c.n_live = at<int32_t>(workspace, pl.n_live);
+    c.part = at<float>(workspace, pl.part);
+    c.num_sms = num_sms_current();
+    c.ws = (WsHeader*)workspace;
+    return cuda_status(launch_embedding_backward(c, (cudaStream_t)stream));
+}
+
+int moe_token_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld, float scale,
+                       const void* targets, int id_bytes, float* logp, float* entropy, float* stats, int n_top,
+                       int32_t* top_idx, float* top_logp, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_logits(dtype, T, V, scale);
+    if (rc) return rc;
+    if (n_top < 0 || n_top > V || (targets != nullptr) != (logp != nullptr)) return MOE_ERR_INVALID_ARG;
+    if (n_top > kMaxTop) return MOE_ERR_UNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    if (!rows_ok(logits, dtype, T, V, ld) || (targets && !ids_ok(targets, id_bytes)) ||
+        (n_top && (!top_idx || !top_logp)))
+        return MOE_ERR_INVALID_ARG;
+    if (((uintptr_t)logp | (uintptr_t)entropy | (uintptr_t)stats | (uintptr_t)top_idx | (uintptr_t)top_logp) & 3)
+        return MOE_ERR_INVALID_ARG;
+    rc = check_status_ws(workspace, workspace_bytes);
+    if (rc) return rc;
+    LogprobCall c{};
+    c.logits = logits;
+    c.dtype = dtype;
+    c.T = T;
+    c.V = V;
+    c.ld = ld;
+    c.scale = scale;
+    c.targets = targets;
+    c.id_bytes = targets ? id_bytes : 4;
+    c.logp = logp;
+    c.entropy = entropy;
+    c.stats = stats;
+    c.n_top = n_top;
+    c.top_idx = top_idx;
+    c.top_logp = top_logp;
+    c.num_sms = num_sms_current();
+    c.ws = (WsHeader*)workspace;
+    return cuda_status(launch_token_logprobs(c, (cudaStream_t)stream));
+}
+
+int moe_token_logprobs_backward(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld, float scale,
+                                const void* targets, int id_bytes, const float* stats, const float* entropy,
+                                const float* g_logp, const float* g_entropy, void* dlogits, int64_t ld_dlogits,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_logits(dtype, T, V, scale);
+    if (rc) return rc;
+    if ((!g_logp && !g_entropy) || (g_logp && !targets) || (g_entropy && !entropy)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!rows_ok(logits, dtype, T, V, ld) || !rows_ok(dlogits, dtype, T, V, ld_dlogits) || !stats ||
+        (g_logp && !ids_ok(targets, id_bytes)))
+        return MOE_ERR_INVALID_ARG;
+    if (((uintptr_t)stats | (uintptr_t)entropy | (uintptr_t)g_logp | (uintptr_t)g_entropy) & 3)
+        return MOE_ERR_INVALID_ARG;
+    if (dlogits == logits && ld != ld_dlogits) return MOE_ERR_INVALID_ARG;
+    rc = check_status_ws(workspace, workspace_bytes);
+    if (rc) return rc;
+    LogprobGradCall c{};
+    c.logits = logits;
+    c.dtype = dtype;
+    c.T = T;
+    c.V = V;
+    c.ld = ld;
+    c.scale = scale;
+    c.targets = targets;
+    c.id_bytes = g_logp ? id_bytes : 4;
+    c.stats = stats;
+    c.entropy = entropy;
+    c.g_logp = g_logp;
+    c.g_entropy = g_entropy;
+    c.dlogits = dlogits;
+    c.ld_d = ld_dlogits;
+    c.num_sms = num_sms_current();
+    c.ws = (WsHeader*)workspace;
+    return cuda_status(launch_token_logprobs_backward(c, (cudaStream_t)stream));
+}
+
+int moe_dropout(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld_x, const void* residual,
+                int64_t ld_residual, double p, uint64_t seed, uint64_t offset, void* out, int64_t ld_out,
+                void* stream) {
+    if (rows < 0 || cols < 0 || !(p >= 0.0 && p <= 1.0)) return MOE_ERR_INVALID_ARG;
+    if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return MOE_OK;
+    if (!rows_ok(x, dtype, rows, cols, ld_x) || !rows_ok(out, dtype, rows, cols, ld_out) ||
+        (residual && !rows_ok(residual, dtype, rows, cols, ld_residual)))
+        return MOE_ERR_INVALID_ARG;
+    if ((x == out && ld_x != ld_out) || (residual == out && ld_residual != ld_out)) return MOE_ERR_INVALID_ARG;
+    const uint32_t thr = (uint32_t)llrint(p * 65536.0);
+    return cuda_status(launch_dropout(x, dtype, rows, cols, ld_x, residual, ld_residual, thr, seed, offset, out,
+                                      ld_out, num_sms_current(), (cudaStream_t)stream));
 }
 
 }  // extern "C"

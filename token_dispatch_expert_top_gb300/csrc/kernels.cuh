@@ -205,6 +205,72 @@ struct FfnMaps {
 struct GemmSide;
 bool encode_ffn_maps(const TcFfnCall& c, FfnMaps* m, GemmSide* s1, GemmSide* s2);
 
+// Token embedding and its gradient (embedding.cu).
+cudaError_t launch_embedding(const void* ids, int id_bytes, int64_t N, const void* table, int table_dtype, int64_t V,
+                             int64_t H, int64_t ld_table, float scale, void* out, int out_dtype, int64_t ld_out,
+                             int num_sms, WsHeader* ws, cudaStream_t stream);
+constexpr int kEmbedRange = 32;    // sorted tokens per range of the gradient's sums (one per lane)
+inline int embed_ranges(int64_t N) { return (int)((N + kEmbedRange - 1) / kEmbedRange); }
+struct EmbedBackward {
+    const void* ids;
+    int id_bytes;
+    int64_t N, V, H;
+    const void* dout;
+    int dout_dtype;
+    int64_t ld_dout;
+    float scale;
+    void* dtable;
+    int dtable_dtype;
+    int64_t ld_dtable;
+    int accumulate;
+    int32_t* order;           // [N] scratch: tokens sorted by (id, token)
+    int32_t* key;             // [N] scratch: their ids
+    int32_t* n_live;          // [1] scratch: how many have an id
+    float* part;              // [2 ranges][H rounded up to 8] scratch
+    int num_sms;
+    WsHeader* ws;
+};
+cudaError_t launch_embedding_backward(const EmbedBackward& c, cudaStream_t stream);
+
+// Log probabilities of given tokens and their gradient (logprobs.cu).
+constexpr int kMaxLogprobVocab = 1 << 22;
+constexpr int kMaxTop = 32;
+struct LogprobCall {
+    const void* logits;
+    int dtype;
+    int64_t T, V, ld;
+    float scale;
+    const void* targets;      // nullable with logp
+    int id_bytes;
+    float *logp, *entropy, *stats;
+    int n_top;
+    int32_t* top_idx;
+    float* top_logp;
+    int num_sms;
+    WsHeader* ws;
+};
+cudaError_t launch_token_logprobs(const LogprobCall& c, cudaStream_t stream);
+struct LogprobGradCall {
+    const void* logits;
+    int dtype;
+    int64_t T, V, ld;
+    float scale;
+    const void* targets;
+    int id_bytes;
+    const float *stats, *entropy, *g_logp, *g_entropy;
+    void* dlogits;
+    int64_t ld_d;
+    int num_sms;
+    WsHeader* ws;
+};
+cudaError_t launch_token_logprobs_backward(const LogprobGradCall& c, cudaStream_t stream);
+
+// Dropout from a counter-based generator with the residual add (dropout.cu); thr of 65536
+// drops everything.
+cudaError_t launch_dropout(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld_x, const void* residual,
+                           int64_t ld_res, uint32_t thr, uint64_t seed, uint64_t offset, void* out, int64_t ld_out,
+                           int num_sms, cudaStream_t stream);
+
 // Shape validation shared by the entry points (api.cu): MOE_OK or the status to
 // return before anything is launched.
 int validate_shape(const moe_shape_t* s);

@@ -1,0 +1,82 @@
+// vec_io.cuh -- groups of eight consecutive FP32 or BF16 elements as FP32 registers:
+// the unit in which the operators around the layer (embedding.cu, logprobs.cu,
+// dropout.cu) move rows.  VECTOR: the group is 16-byte aligned and whole (one 16-byte
+// access for BF16, two for FP32); otherwise element by element, `n` of the eight.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+// Element types by moe_dtype_t; BF16 travels as its 16 bits.
+template <typename T>
+__device__ __forceinline__ float to_f32(T v) {
+    if constexpr (sizeof(T) == 2) return bf16_to_f32(v);
+    else return v;
+}
+template <typename T>
+__device__ __forceinline__ T from_f32(float v) {
+    if constexpr (sizeof(T) == 2) return f32_to_bf16_rn(v);
+    else return v;
+}
+
+__device__ __forceinline__ void unpack_bf16x8(const uint4& q, float* v) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        v[2 * p] = __uint_as_float(w[p] << 16);
+        v[2 * p + 1] = __uint_as_float(w[p] & 0xFFFF0000u);
+    }
+}
+
+// 16-byte load past L1 through the coherent path: an operator may write the buffer it reads
+// (each thread its own elements, after reading them).
+__device__ __forceinline__ uint4 ld_v4(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+template <typename T, bool VECTOR>
+__device__ __forceinline__ void load8(const T* p, int n, float* v) {
+    if constexpr (VECTOR && sizeof(T) == 2) {
+        unpack_bf16x8(ld_v4(p), v);
+    } else if constexpr (VECTOR) {
+        const uint4 a = ld_v4(p), b = ld_v4(p + 4);
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f32<T>(p[i]) : 0.f;
+    }
+}
+
+template <typename T, bool VECTOR>
+__device__ __forceinline__ void store8(T* p, int n, const float* v) {
+    if constexpr (VECTOR && sizeof(T) == 2) {
+        st_v4(p, make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                            pack_bf16x2(v[6], v[7])));
+    } else if constexpr (VECTOR) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 4)
+            st_v4(p + i, make_uint4(__float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]),
+                                    __float_as_uint(v[i + 3])));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = from_f32<T>(v[i]);
+    }
+}
+
+inline size_t dtype_bytes(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
+
+// Whether rows of `cols` elements, `ld` apart, split into whole 16-byte aligned groups of
+// eight.
+inline bool rows_in_groups(const void* base, int64_t cols, int64_t ld, int dtype) {
+    return cols % 8 == 0 && ((uintptr_t)base & 15) == 0 && (ld * (int64_t)dtype_bytes(dtype)) % 16 == 0;
+}
+
+}  // namespace moe

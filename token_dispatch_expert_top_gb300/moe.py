@@ -31,6 +31,8 @@ ENTRY_POINTS = (
     "moe_pack_expert_weights", "moe_backward_workspace_bytes", "moe_pack_expert_weights_dgrad",
     "moe_expert_ffn_train", "moe_forward_train", "moe_reverse_combine", "moe_expert_ffn_dgrad",
     "moe_reverse_dispatch", "moe_router_wgrad", "moe_backward", "moe_expert_wgrad",
+    "moe_embedding", "moe_embedding_workspace_bytes", "moe_embedding_backward", "moe_token_logprobs",
+    "moe_token_logprobs_backward", "moe_dropout",
 )
 
 
@@ -77,6 +79,7 @@ def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
 
 _lib = load_library()
 _vp, _i, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+_f32, _f64, _u64 = ctypes.c_float, ctypes.c_double, ctypes.c_uint64
 _shp, _prm, _svd = ctypes.POINTER(Shape), ctypes.POINTER(Params), ctypes.POINTER(Saved)
 _SIGS = {
     "moe_workspace_bytes": (_sz, [_shp, _prm]),
@@ -112,6 +115,15 @@ _SIGS = {
     "moe_backward": (_i, [_vp, _vp, _vp, _svd, _vp, _vp, _vp, _vp, _shp, _prm, _vp, _vp, _vp, _vp,
                           _vp, _vp, _sz, _vp]),
     "moe_expert_wgrad": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _shp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_embedding": (_i, [_vp, _i, _i64, _vp, _i, _i64, _i64, _i64, _f32, _vp, _i, _i64, _vp, _sz, _vp]),
+    "moe_embedding_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "moe_embedding_backward": (_i, [_vp, _i, _i64, _i64, _i64, _vp, _i, _i64, _f32, _vp, _i, _i64, _i, _vp, _sz,
+                                    _vp]),
+    "moe_token_logprobs": (_i, [_vp, _i, _i64, _i64, _i64, _f32, _vp, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp, _sz,
+                                _vp]),
+    "moe_token_logprobs_backward": (_i, [_vp, _i, _i64, _i64, _i64, _f32, _vp, _i, _vp, _vp, _vp, _vp, _vp, _i64,
+                                         _vp, _sz, _vp]),
+    "moe_dropout": (_i, [_vp, _i, _i64, _i64, _i64, _vp, _i64, _f64, _u64, _u64, _vp, _i64, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -339,3 +351,126 @@ def moe_backward(dout, x, w_router, saved: Saved, wt_gate_up, wt_gu_scales, wt_d
         _p(wt_down), _p(wt_d_scales), ctypes.byref(shape), ctypes.byref(params) if params else None,
         _p(dx), _p(dw_router), _p(dbias), _p(dw_gate_up), _p(dw_down), _p(ws), _wsz(ws),
         _stream(stream)))
+
+
+# ------------------------------------------------------------------ operators around the layer
+_FLOAT_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+_ID_BYTES = {torch.int32: 4, torch.int64: 8}
+
+
+def _rows(fn: str, name: str, t: torch.Tensor) -> tuple[int, int, int, int, int]:
+    """(pointer, moe dtype, rows, columns, row stride in elements) of a matrix whose rows
+    are contiguous; leading dimensions that lie row after row count as rows."""
+    dt = _FLOAT_DTYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{fn}: {name} is {t.dtype}; float32 or bfloat16 is wanted")
+    if not t.is_cuda:
+        raise ValueError(f"{fn}: {name} is not on a CUDA device")
+    if t.dim() != 2:
+        if t.dim() == 0:
+            raise ValueError(f"{fn}: {name} has no columns")
+        t = t.view(-1, t.shape[-1])
+    rows, cols = t.shape
+    ld = t.stride(0)
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{fn}: the rows of {name} are not contiguous")
+    return t.data_ptr(), dt, rows, cols, ld if rows > 1 else max(ld, cols)
+
+
+def _ids(fn: str, name: str, t: torch.Tensor, n: int) -> tuple[int, int]:
+    """(pointer, bytes per id) of n contiguous token ids."""
+    size = _ID_BYTES.get(t.dtype)
+    if size is None:
+        raise TypeError(f"{fn}: {name} is {t.dtype}; int32 or int64 is wanted")
+    _vector(fn, name, t, t.dtype, n)
+    return t.data_ptr(), size
+
+
+def _vector(fn: str, name: str, t: torch.Tensor, dtype: torch.dtype, n: int) -> None:
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{fn}: {name} has to be {n} contiguous elements of {dtype} on a CUDA device")
+
+
+def moe_embedding(ids, table, out, scale: float = 1.0, ws=None, stream=None) -> None:
+    """out[n] = scale * table[ids[n]]; out: [..., H], one row per id."""
+    fn = "moe_embedding"
+    tp, td, V, H, tl = _rows(fn, "table", table)
+    op, od, N, oh, ol = _rows(fn, "out", out)
+    if oh != H:
+        raise ValueError(f"{fn}: out has {oh} columns, table {H}")
+    ip, isz = _ids(fn, "ids", ids, N)
+    _check(fn, _lib.moe_embedding(ip, isz, N, tp, td, V, H, tl, scale, op, od, ol, _p(ws), _wsz(ws),
+                                  _stream(stream)))
+
+
+def moe_embedding_workspace_bytes(N: int, V: int, H: int) -> int:
+    return _lib.moe_embedding_workspace_bytes(N, V, H)
+
+
+def moe_embedding_backward(ids, dout, dtable, scale: float = 1.0, accumulate: bool = False, ws=None,
+                           stream=None) -> None:
+    """dtable[v] (+)= scale * sum of dout's rows whose id is v."""
+    fn = "moe_embedding_backward"
+    gp, gd, N, gh, gl = _rows(fn, "dout", dout)
+    tp, td, V, H, tl = _rows(fn, "dtable", dtable)
+    if gh != H:
+        raise ValueError(f"{fn}: dout has {gh} columns, dtable {H}")
+    ip, isz = _ids(fn, "ids", ids, N)
+    _check(fn, _lib.moe_embedding_backward(ip, isz, N, V, H, gp, gd, gl, scale, tp, td, tl, accumulate, _p(ws),
+                                           _wsz(ws), _stream(stream)))
+
+
+def moe_token_logprobs(logits, targets=None, logp=None, entropy=None, stats=None, top_idx=None, top_logp=None,
+                       scale: float = 1.0, ws=None, stream=None) -> None:
+    """Log probability of each row's target, entropy, the gradient's statistics and the
+    top list, each into the tensor given for it (None: not computed)."""
+    fn = "moe_token_logprobs"
+    lp, dt, T, V, ld = _rows(fn, "logits", logits)
+    tp, isz = (None, 4) if targets is None else _ids(fn, "targets", targets, T)
+    n_top = 0
+    if top_idx is not None and top_logp is not None:
+        n_top = top_idx.shape[-1]
+        _vector(fn, "top_idx", top_idx, torch.int32, T * n_top)
+        _vector(fn, "top_logp", top_logp, torch.float32, T * n_top)
+    elif top_idx is not None or top_logp is not None:
+        raise ValueError(f"{fn}: top_idx and top_logp are given together")
+    for name, t, n in (("logp", logp, T), ("entropy", entropy, T), ("stats", stats, 2 * T)):
+        if t is not None:
+            _vector(fn, name, t, torch.float32, n)
+    _check(fn, _lib.moe_token_logprobs(lp, dt, T, V, ld, scale, tp, isz, _p(logp), _p(entropy), _p(stats), n_top,
+                                       _p(top_idx) if n_top else None, _p(top_logp) if n_top else None, _p(ws),
+                                       _wsz(ws), _stream(stream)))
+
+
+def moe_token_logprobs_backward(logits, targets, stats, entropy, g_logp, g_entropy, dlogits, scale: float = 1.0,
+                                ws=None, stream=None) -> None:
+    """dlogits of moe_token_logprobs; dlogits may be logits itself."""
+    fn = "moe_token_logprobs_backward"
+    lp, dt, T, V, ld = _rows(fn, "logits", logits)
+    dp, dd, dT, dV, dl = _rows(fn, "dlogits", dlogits)
+    if (dd, dT, dV) != (dt, T, V):
+        raise ValueError(f"{fn}: dlogits has to have logits' type and shape")
+    tp, isz = (None, 4) if targets is None else _ids(fn, "targets", targets, T)
+    for name, t, n in (("stats", stats, 2 * T), ("entropy", entropy, T), ("g_logp", g_logp, T),
+                       ("g_entropy", g_entropy, T)):
+        if t is not None:
+            _vector(fn, name, t, torch.float32, n)
+    _check(fn, _lib.moe_token_logprobs_backward(lp, dt, T, V, ld, scale, tp, isz, _p(stats), _p(entropy), _p(g_logp),
+                                                _p(g_entropy), dp, dl, _p(ws), _wsz(ws), _stream(stream)))
+
+
+def moe_dropout(x, out, p: float, seed: int, offset: int = 0, residual=None, stream=None) -> None:
+    """out = residual + dropout(x); out may be x or residual."""
+    fn = "moe_dropout"
+    xp, dt, rows, cols, ld = _rows(fn, "x", x)
+    op, od, orows, ocols, ol = _rows(fn, "out", out)
+    rp, rl = None, 0
+    if residual is not None:
+        rp, rd, rrows, rcols, rl = _rows(fn, "residual", residual)
+        if (rd, rrows, rcols) != (dt, rows, cols):
+            raise ValueError(f"{fn}: residual has to have x's type and shape")
+    if (od, orows, ocols) != (dt, rows, cols):
+        raise ValueError(f"{fn}: out has to have x's type and shape")
+    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+        raise ValueError(f"{fn}: seed and offset are unsigned 64-bit numbers")
+    _check(fn, _lib.moe_dropout(xp, dt, rows, cols, ld, rp, rl, p, seed, offset, op, ol, _stream(stream)))
