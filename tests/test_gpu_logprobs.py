@@ -157,6 +157,20 @@ def test_masks_ties_and_orders(M, dtype, T):
     _check(M, x, t, 0.5, 7)
 
 
+@pytest.mark.parametrize("T", [1, 40, 700])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_one_logit_left_is_certain(M, T, dtype):
+    """A distribution of one token: log probability and entropy exactly 0."""
+    V = 3333
+    x = torch.full((T, V), -INF, dtype=dtype, device="cuda")
+    t = _targets(T, V)
+    x[torch.arange(T, device="cuda"), t] = torch.randn(T, device="cuda").mul_(20).to(dtype)
+    for scale in (1.0, 0.7, 1.25):
+        o = _forward(M, x, t, scale, 3)
+        assert not o["logp"].any() and not o["entropy"].any()
+        assert torch.equal(o["top_idx"][:, 0].long(), t) and not o["top_logp"][:, 0].any()
+
+
 def test_extreme_values(M):
     """Logits of up to the largest finite values, both signs; probabilities that underflow."""
     x = torch.zeros((4, 600), device="cuda")

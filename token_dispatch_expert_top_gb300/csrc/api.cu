@@ -283,10 +283,10 @@ int check_status_ws(void* ws, size_t bytes) {
 
 // Workspace regions of moe_embedding_backward, in order.
 struct EmbedPlan {
-    size_t n_live, order, key, part, total;
+    size_t n_live, order, key, present, part, total;
 };
 
-EmbedPlan make_embed_plan(int64_t N, int64_t H) {
+EmbedPlan make_embed_plan(int64_t N, int64_t V, int64_t H) {
     EmbedPlan pl{};
     size_t off = align256(sizeof(WsHeader));
     auto take = [&](size_t bytes) {
@@ -297,7 +297,8 @@ EmbedPlan make_embed_plan(int64_t N, int64_t H) {
     pl.n_live = take(sizeof(int32_t));
     pl.order = take(sizeof(int32_t) * (size_t)N);
     pl.key = take(sizeof(int32_t) * (size_t)N);
-    pl.part = take(sizeof(float) * 2 * (size_t)embed_ranges(N) * (size_t)((H + 7) / 8 * 8));
+    pl.present = take(sizeof(uint32_t) * (size_t)((V + 31) / 32));
+    pl.part = take(sizeof(float) * 2 * (size_t)embed_ranges(N, H) * (size_t)((H + 7) / 8 * 8));
     pl.total = off;
     return pl;
 }
@@ -1068,12 +1069,12 @@ int moe_embedding(const void* ids, int id_bytes, int64_t N, const void* table, i
     rc = check_status_ws(workspace, workspace_bytes);
     if (rc) return rc;
     return cuda_status(launch_embedding(ids, id_bytes, N, table, table_dtype, V, H, ld_table, scale, out, out_dtype,
-                                        ld_out, num_sms_current(), (WsHeader*)workspace, (cudaStream_t)stream));
+                                        ld_out, (WsHeader*)workspace, (cudaStream_t)stream));
 }
 
 size_t moe_embedding_workspace_bytes(int64_t N, int64_t V, int64_t H) {
     if (check_embed_shape(N, V, H) != MOE_OK) return 0;
-    return make_embed_plan(N, H).total;
+    return make_embed_plan(N, V, H).total;
 }
 
 int moe_embedding_backward(const void* ids, int id_bytes, int64_t N, int64_t V, int64_t H, const void* dout,
@@ -1086,7 +1087,7 @@ int moe_embedding_backward(const void* ids, int id_bytes, int64_t N, int64_t V, 
     if (!rows_ok(dtable, dtable_dtype, V, H, ld_dtable)) return MOE_ERR_INVALID_ARG;
     if (N == 0 && accumulate) return MOE_OK;
     if (N > 0 && (!ids_ok(ids, id_bytes) || !rows_ok(dout, dout_dtype, N, H, ld_dout))) return MOE_ERR_INVALID_ARG;
-    const EmbedPlan pl = make_embed_plan(N, H);
+    const EmbedPlan pl = make_embed_plan(N, V, H);
     if (!workspace || ((uintptr_t)workspace & 31) || workspace_bytes < pl.total) return MOE_ERR_WORKSPACE;
     EmbedBackward c{};
     c.ids = ids;
@@ -1105,6 +1106,7 @@ int moe_embedding_backward(const void* ids, int id_bytes, int64_t N, int64_t V, 
     c.order = at<int32_t>(workspace, pl.order);
     c.key = at<int32_t>(workspace, pl.key);
     c.n_live = at<int32_t>(workspace, pl.n_live);
+    c.present = at<uint32_t>(workspace, pl.present);
     c.part = at<float>(workspace, pl.part);
     c.num_sms = num_sms_current();
     c.ws = (WsHeader*)workspace;
@@ -1194,7 +1196,7 @@ int moe_dropout(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld
     if ((x == out && ld_x != ld_out) || (residual == out && ld_residual != ld_out)) return MOE_ERR_INVALID_ARG;
     const uint32_t thr = (uint32_t)llrint(p * 65536.0);
     return cuda_status(launch_dropout(x, dtype, rows, cols, ld_x, residual, ld_residual, thr, seed, offset, out,
-                                      ld_out, num_sms_current(), (cudaStream_t)stream));
+                                      ld_out, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -8,12 +8,12 @@
 // values, so it is deterministic:
 //   1. embed_order_kernel: each CTA owns a range of ids, reads all N ids (they stay in L2),
 //      counts its own and how many live ids lie below its range, and places its tokens in
-//      ascending token order -- no exchange between CTAs.  Rows no token names are set to
-//      zero here (unless the caller accumulates).
-//   2. embed_segment_kernel: the sorted list is cut into ranges of Q tokens whatever the
+//      ascending token order -- no exchange between CTAs.
+//   2. embed_segment_kernel: the sorted list is cut into ranges of 4 to 32 tokens whatever the
 //      ids, so a frequent token cannot unbalance it; a run of equal ids inside a range is
 //      summed in FP32 in token order and written, a run that crosses a range's end leaves
-//      an FP32 partial row.
+//      an FP32 partial row.  (Before it embed_fill_kernel sets the rows no token names to
+//      zero, unless the caller accumulates.)
 //   3. embed_join_kernel: adds the partial rows of each run that crossed, in order.
 #include "kernels.cuh"
 #include "vec_io.cuh"
@@ -32,91 +32,155 @@ __device__ __forceinline__ int live_id(Id id, int64_t V, bool* bad) {
 }
 
 // ------------------------------------------------------------------------ forward
-// One thread per group of eight columns of an output row, four groups a round with
-// their loads issued first.
+// Eight columns of a row in a lane's registers.  VECTOR: eight neighbours, by 16-byte
+// accesses; otherwise every 32nd column, so that the warp's lanes touch neighbouring elements
+// whatever the alignment.  Both cover the warp's 256 columns from c0.
+template <typename T, bool VECTOR>
+__device__ __forceinline__ void load_cols(const T* row, int64_t c0, int lane, int64_t H, float* v) {
+    if constexpr (VECTOR) {
+        if (c0 + lane * 8 < H) load8<T, true>(row + c0 + lane * 8, 8, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c0 + i * 32 + lane < H ? to_f32<T>(row[c0 + i * 32 + lane]) : 0.f;
+    }
+}
+template <typename T, bool VECTOR>
+__device__ __forceinline__ void store_cols(T* row, int64_t c0, int lane, int64_t H, const float* v) {
+    if constexpr (VECTOR) {
+        if (c0 + lane * 8 < H) store8<T, true>(row + c0 + lane * 8, 8, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c0 + i * 32 + lane < H) row[c0 + i * 32 + lane] = from_f32<T>(v[i]);
+    }
+}
+
+// The same eight columns as they lie in memory, converted when they are used: half the
+// registers for BF16 rows in flight.
+template <typename T, bool VECTOR>
+struct RawCols {
+    static constexpr bool kPacked = VECTOR && sizeof(T) == 2;
+    uint4 q;
+    float v[kPacked ? 1 : 8];
+    __device__ void load(const T* row, int64_t c0, int lane, int64_t H) {
+        if constexpr (kPacked) {
+            if (c0 + lane * 8 < H) q = ld_v4(row + c0 + lane * 8);
+        } else {
+            load_cols<T, VECTOR>(row, c0, lane, H, v);
+        }
+    }
+    __device__ void add_to(float* sum) const {
+        if constexpr (kPacked) {
+            float x[8];
+            unpack_bf16x8(q, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] += x[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] += v[j];
+        }
+    }
+};
+
+// A memory-bound copy with a scale.  Short rows (aligned, at most 128 columns): 2^lane_bits
+// lanes per row, each one group of eight columns.  Otherwise one warp per 256 * U columns of
+// a row; its loads are all issued before the first store.
+constexpr int kEmbedUnroll = 4;
 template <typename Id, typename In, typename Out, bool VECTOR>
 __global__ void __launch_bounds__(256) embedding_kernel(const Id* __restrict__ ids, int64_t N,
                                                         const In* __restrict__ table, int64_t V, int64_t H,
                                                         int64_t ld_table, float scale, Out* __restrict__ out,
-                                                        int64_t ld_out, WsHeader* ws) {
-    constexpr int U = 4;
-    const int64_t groups = (H + 7) / 8;
-    const int64_t total = N * groups;
-    const int64_t step = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t g0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; g0 < total; g0 += U * step) {
-        float v[U][8];
+                                                        int64_t ld_out, int chunks, int lane_bits, WsHeader* ws) {
+    const int lane = threadIdx.x % 32;
+    const uint64_t item = (uint64_t)blockIdx.x * 8 + threadIdx.x / 32;
+    if (lane_bits < 5) {
+        const int64_t n = (int64_t)(item << (5 - lane_bits)) + (lane >> lane_bits);
+        const int64_t c = (lane & ((1 << lane_bits) - 1)) * 8;
+        if (n >= N || c >= H) return;
+        bool bad = false;
+        const int id = live_id(ids[n], V, &bad);
+        if (bad && c == 0) set_status(ws, MOE_ERR_DEVICE_CHECK);
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (id >= 0) load8<In, true>(table + id * ld_table + c, 8, v);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t g = g0 + u * step;
+        for (int i = 0; i < 8; ++i) v[i] *= scale;
+        store8<Out, true>(out + n * ld_out + c, 8, v);
+        return;
+    }
+    const int64_t n = item >> 32 ? (int64_t)(item / (uint32_t)chunks) : (int64_t)((uint32_t)item / (uint32_t)chunks);
+    if (n >= N) return;
+    const int64_t c0 = (int64_t)(item - (uint64_t)n * chunks) * (256 * kEmbedUnroll);
+    bool bad = false;
+    const int id = live_id(ids[n], V, &bad);
+    if (bad && lane == 0 && c0 == 0) set_status(ws, MOE_ERR_DEVICE_CHECK);
+    float v[kEmbedUnroll][8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
-            if (g >= total) continue;
-            const int64_t n = g / groups, c = (g % groups) * 8;
-            bool bad = false;
-            const int id = live_id(ids[n], V, &bad);
-            if (bad && c == 0) set_status(ws, MOE_ERR_DEVICE_CHECK);
-            if (id >= 0) load8<In, VECTOR>(table + id * ld_table + c, (int)(H - c < 8 ? H - c : 8), v[u]);
-        }
+    for (int u = 0; u < kEmbedUnroll; ++u) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t g = g0 + u * step;
-            if (g >= total) continue;
-            const int64_t n = g / groups, c = (g % groups) * 8;
+        for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
+        if (id >= 0) load_cols<In, VECTOR>(table + id * ld_table, c0 + u * 256, lane, H, v[u]);
+    }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[u][i] *= scale;
-            store8<Out, VECTOR>(out + n * ld_out + c, (int)(H - c < 8 ? H - c : 8), v[u]);
-        }
+    for (int u = 0; u < kEmbedUnroll; ++u) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] *= scale;
+        store_cols<Out, VECTOR>(out + n * ld_out, c0 + u * 256, lane, H, v[u]);
     }
 }
 
 template <typename Id, typename In, typename Out>
 static cudaError_t launch_embedding_t(const void* ids, int64_t N, const void* table, int64_t V, int64_t H,
                                       int64_t ld_table, float scale, void* out, int64_t ld_out, bool vec,
-                                      int num_sms, WsHeader* ws, cudaStream_t stream) {
-    const int64_t total = N * ((H + 7) / 8);
-    int64_t grid = (total + 255) / 256;
-    if (grid > (int64_t)num_sms * 8) grid = (int64_t)num_sms * 8;
+                                      WsHeader* ws, cudaStream_t stream) {
+    int lane_bits = 5;
+    if (vec && H <= 128)
+        for (lane_bits = 0; (8 << lane_bits) < H;) ++lane_bits;
+    const int64_t chunks = lane_bits < 5 ? 1 : (H + 256 * kEmbedUnroll - 1) / (256 * kEmbedUnroll);
+    const int64_t items = lane_bits < 5 ? (N + (32 >> lane_bits) - 1) >> (5 - lane_bits) : N * chunks;
+    const int64_t grid = (items + 7) / 8;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     auto* k = vec ? embedding_kernel<Id, In, Out, true> : embedding_kernel<Id, In, Out, false>;
     k<<<(unsigned)grid, 256, 0, stream>>>((const Id*)ids, N, (const In*)table, V, H, ld_table, scale, (Out*)out,
-                                          ld_out, ws);
+                                          ld_out, (int)chunks, lane_bits, ws);
     return cudaGetLastError();
 }
 
 template <typename Id>
 static cudaError_t launch_embedding_id(const void* ids, int64_t N, const void* table, int table_dtype, int64_t V,
                                        int64_t H, int64_t ld_table, float scale, void* out, int out_dtype,
-                                       int64_t ld_out, int num_sms, WsHeader* ws, cudaStream_t stream) {
+                                       int64_t ld_out, WsHeader* ws, cudaStream_t stream) {
     const bool vec = rows_in_groups(table, H, ld_table, table_dtype) && rows_in_groups(out, H, ld_out, out_dtype);
     if (table_dtype == MOE_F32)
         return out_dtype == MOE_F32
                    ? launch_embedding_t<Id, float, float>(ids, N, table, V, H, ld_table, scale, out, ld_out, vec,
-                                                          num_sms, ws, stream)
+                                                          ws, stream)
                    : launch_embedding_t<Id, float, uint16_t>(ids, N, table, V, H, ld_table, scale, out, ld_out, vec,
-                                                             num_sms, ws, stream);
+                                                             ws, stream);
     return out_dtype == MOE_F32
                ? launch_embedding_t<Id, uint16_t, float>(ids, N, table, V, H, ld_table, scale, out, ld_out, vec,
-                                                         num_sms, ws, stream)
+                                                         ws, stream)
                : launch_embedding_t<Id, uint16_t, uint16_t>(ids, N, table, V, H, ld_table, scale, out, ld_out, vec,
-                                                            num_sms, ws, stream);
+                                                            ws, stream);
 }
 
 cudaError_t launch_embedding(const void* ids, int id_bytes, int64_t N, const void* table, int table_dtype, int64_t V,
                              int64_t H, int64_t ld_table, float scale, void* out, int out_dtype, int64_t ld_out,
-                             int num_sms, WsHeader* ws, cudaStream_t stream) {
+                             WsHeader* ws, cudaStream_t stream) {
     if (N == 0) return cudaSuccess;
     return id_bytes == 8 ? launch_embedding_id<int64_t>(ids, N, table, table_dtype, V, H, ld_table, scale, out,
-                                                        out_dtype, ld_out, num_sms, ws, stream)
+                                                        out_dtype, ld_out, ws, stream)
                          : launch_embedding_id<int32_t>(ids, N, table, table_dtype, V, H, ld_table, scale, out,
-                                                        out_dtype, ld_out, num_sms, ws, stream);
+                                                        out_dtype, ld_out, ws, stream);
 }
 
 // ------------------------------------------------------------------------ order
-constexpr int kOrderThreads = 512;
-constexpr int kOrderTile = kOrderThreads;     // ids placed per round
+constexpr int kOrderThreads = 1024;
+constexpr int kOrderIds = 4;                  // ids a thread reads per sweep of the CTA
+constexpr int kOrderList = 4096;              // own tokens kept in shared memory
 
 // Exclusive prefix sum over the CTA's threads; *total is the sum.  All threads call it.
 __device__ __forceinline__ int block_scan_exclusive(int v, int* warp_sums, int* total) {
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     int incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -126,175 +190,279 @@ __device__ __forceinline__ int block_scan_exclusive(int v, int* warp_sums, int* 
     __syncthreads();                          // earlier reads of warp_sums are done
     if (lane == 31) warp_sums[warp] = incl;
     __syncthreads();
-    int before = 0, all = 0;
-    for (int w = 0; w < warps; ++w) {
-        const int s = warp_sums[w];
-        if (w < warp) before += s;
-        all += s;
-    }
-    *total = all;
+    int s = warp_sums[lane];                  // kOrderThreads / 32 = 32 warps
+    int before = lane < warp ? s : 0;
+    before = __reduce_add_sync(0xffffffffu, before);
+    *total = __reduce_add_sync(0xffffffffu, s);
     return before + incl - v;
 }
 
+// The sorted list's places for the CTA's own tokens list_row / list_pos [0, n), which are in
+// token order: by one warp, 32 at a time; cursor[row] is the row's next place.
+__device__ __forceinline__ void place_list(const int* list_row, const int* list_pos, int n, int* cursor, int v0,
+                                           int32_t* order, int32_t* key) {
+    const int lane = threadIdx.x % 32;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + lane;
+        const int row = i < n ? list_row[i] : -1 - lane;
+        const unsigned same = __match_any_sync(0xffffffffu, row);
+        if (row >= 0) {
+            const int place = cursor[row] + __popc(same & ((1u << lane) - 1u));
+            order[place] = list_pos[i];
+            key[place] = v0 + row;
+        }
+        __syncwarp();
+        if (row >= 0 && lane == 31 - __clz(same)) cursor[row] += __popc(same);
+        __syncwarp();
+    }
+}
+
 // CTA b places the tokens whose ids lie in [b * range, (b + 1) * range): order[i] is the
-// token at place i of the list sorted by (id, token), key[i] its id.  cursor: `range` ints of
-// shared memory.
-template <typename Id, typename Grad, bool VECTOR>
+// token at place i of the list sorted by (id, token), key[i] its id; bit v of `present` says
+// that a token names v.  range is a multiple of 32.  Shared memory: `range` counters.
+//   One sweep over the ids counts the CTA's own tokens by id, counts the live tokens below
+// its range (where its part of the list begins) and lists its own tokens in order; if the
+// list overflows, a second sweep places them piece by piece.
+template <typename Id>
 __global__ void __launch_bounds__(kOrderThreads)
     embed_order_kernel(const Id* __restrict__ ids, int N, int64_t V, int range, int32_t* __restrict__ order,
-                       int32_t* __restrict__ key, int32_t* __restrict__ n_live, Grad* __restrict__ dtable, int64_t H,
-                       int64_t ld, int fill, WsHeader* ws) {
+                       int32_t* __restrict__ key, int32_t* __restrict__ n_live, uint32_t* __restrict__ present,
+                       WsHeader* ws) {
+    grid_dependents_launch();
     extern __shared__ int cursor[];
     __shared__ int warp_sums[kOrderThreads / 32];
-    __shared__ int list_row[kOrderTile], list_pos[kOrderTile];
+    __shared__ int list_row[kOrderList], list_pos[kOrderList];
+    constexpr int kSweep = kOrderThreads * kOrderIds;
+    static_assert(kSweep <= kOrderList, "a sweep's own tokens fit the list");
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    const int64_t v0 = (int64_t)blockIdx.x * range;
+    const int v0 = (int)((int64_t)blockIdx.x * range);
     const int rows = (int)(V - v0 < range ? V - v0 : range);
     for (int i = tid; i < rows; i += kOrderThreads) cursor[i] = 0;
+    // ids[n0 + kOrderIds * tid ..], -1 past the end
+    auto read_ids = [&](int n0, int (&id)[kOrderIds], bool* bad) {
+#pragma unroll
+        for (int i = 0; i < kOrderIds; ++i) {
+            const int n = n0 + tid * kOrderIds + i;
+            id[i] = n < N ? live_id(ids[n], V, bad) : -1;
+        }
+    };
     __syncthreads();
-    // count this range's tokens by id, and the live tokens below the range
-    int below = 0, live = 0;
+    int below = 0, live = 0, listed = 0;
     bool bad = false;
-    for (int n = tid; n < N; n += kOrderThreads) {
-        const int id = live_id(ids[n], V, &bad);
-        if (id < 0) continue;
-        ++live;
-        if (id < v0) ++below;
-        else if (id < v0 + rows) atomicAdd(&cursor[id - (int)v0], 1);
+    int next[kOrderIds];
+    read_ids(0, next, &bad);
+    for (int n0 = 0; n0 < N; n0 += kSweep) {
+        int id[kOrderIds], mine = 0;
+#pragma unroll
+        for (int i = 0; i < kOrderIds; ++i) id[i] = next[i];
+        if (n0 + kSweep < N) read_ids(n0 + kSweep, next, &bad);
+#pragma unroll
+        for (int i = 0; i < kOrderIds; ++i) {
+            live += id[i] >= 0;
+            below += id[i] >= 0 && id[i] < v0;
+            if (id[i] >= v0 && id[i] < v0 + rows) {
+                ++mine;
+                atomicAdd(&cursor[id[i] - v0], 1);
+            }
+        }
+        int total;
+        int at = listed + block_scan_exclusive(mine, warp_sums, &total);
+        if (listed + total <= kOrderList) {
+#pragma unroll
+            for (int i = 0; i < kOrderIds; ++i)
+                if (id[i] >= v0 && id[i] < v0 + rows) {
+                    list_row[at] = id[i] - v0;
+                    list_pos[at++] = n0 + tid * kOrderIds + i;
+                }
+        }
+        listed += total;
     }
     if (bad && blockIdx.x == 0) set_status(ws, MOE_ERR_DEVICE_CHECK);
     int base, all_live;
     block_scan_exclusive(below, warp_sums, &base);
     block_scan_exclusive(live, warp_sums, &all_live);
     if (blockIdx.x == 0 && tid == 0) *n_live = all_live;
-    // counts -> first places
+    // counts -> first places, and the rows' presence
     __syncthreads();
     int run = base;
     for (int i0 = 0; i0 < rows; i0 += kOrderThreads) {
         const int i = i0 + tid;
         const int c = i < rows ? cursor[i] : 0;
+        const unsigned bits = __ballot_sync(0xffffffffu, c > 0);
+        if (lane == 0 && i < rows) present[((int64_t)v0 + i) / 32] = bits;
         int total;
         const int ex = block_scan_exclusive(c, warp_sums, &total);
         if (i < rows) cursor[i] = run + ex;
         run += total;
     }
     __syncthreads();
-    // place, tile by tile in token order: the tile's own tokens are listed in order, then
-    // one warp gives each its id's next place
-    if (run > base) {
-        for (int n0 = 0; n0 < N; n0 += kOrderTile) {
-            const int n = n0 + tid;
-            bool b2 = false;
-            const int id = n < N ? live_id(ids[n], V, &b2) : -1;
-            const bool mine = id >= v0 && id < v0 + rows;
-            int total;
-            const int at = block_scan_exclusive(mine ? 1 : 0, warp_sums, &total);
-            if (mine) {
-                list_row[at] = id - (int)v0;
-                list_pos[at] = n;
-            }
-            __syncthreads();
-            if (warp == 0) {
-                for (int i0 = 0; i0 < total; i0 += 32) {
-                    const int i = i0 + lane;
-                    const int row = i < total ? list_row[i] : -1 - lane;
-                    const unsigned same = __match_any_sync(0xffffffffu, row);
-                    if (row >= 0) {
-                        const int place = cursor[row] + __popc(same & ((1u << lane) - 1u));
-                        order[place] = list_pos[i];
-                        key[place] = (int)v0 + row;
-                    }
-                    __syncwarp();
-                    if (row >= 0 && lane == 31 - __clz(same)) cursor[row] += __popc(same);
-                    __syncwarp();
-                }
-            }
-            // the next round's scan begins with a barrier before the list is written again
-        }
+    if (listed <= kOrderList) {
+        if (warp == 0) place_list(list_row, list_pos, listed, cursor, v0, order, key);
+        return;
     }
-    if (!fill) return;
-    __syncthreads();
-    // cursor[i] is now the first place after row i: equal neighbours mean no token
-    const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int i = warp; i < rows; i += kOrderThreads / 32) {
-        if (cursor[i] != (i ? cursor[i - 1] : base)) continue;
-        Grad* dst = dtable + (v0 + i) * ld;
-        for (int64_t c = lane * 8; c < H; c += 256)
-            store8<Grad, VECTOR>(dst + c, (int)(H - c < 8 ? H - c : 8), zero);
+    for (int n0 = 0; n0 < N; n0 += kSweep) {
+        int id[kOrderIds], mine = 0;
+        read_ids(n0, id, &bad);
+#pragma unroll
+        for (int i = 0; i < kOrderIds; ++i) mine += id[i] >= v0 && id[i] < v0 + rows;
+        int total;
+        int at = block_scan_exclusive(mine, warp_sums, &total);
+#pragma unroll
+        for (int i = 0; i < kOrderIds; ++i)
+            if (id[i] >= v0 && id[i] < v0 + rows) {
+                list_row[at] = id[i] - v0;
+                list_pos[at++] = n0 + tid * kOrderIds + i;
+            }
+        __syncthreads();
+        if (warp == 0) place_list(list_row, list_pos, total, cursor, v0, order, key);
+        // the next round's scan begins with a barrier before the list is written again
     }
 }
 
 // ------------------------------------------------------------------------ sums
-// Writes scale * sum (+ the row's old value) of the columns c .. c+7 of row v.
+// Writes scale * sum (+ the row's old value) of the warp's 256 columns of row v.
 template <typename Grad, bool VECTOR>
-__device__ __forceinline__ void write_row(Grad* dtable, int64_t ld, int v, int64_t c, int n, const float* sum,
-                                          float scale, int accumulate) {
-    float o[8];
-    Grad* dst = dtable + v * ld + c;
-    if (accumulate) {
-        load8<Grad, VECTOR>(dst, n, o);
+__device__ __forceinline__ void write_row(Grad* dtable, int64_t ld, int v, int64_t c0, int lane, int64_t H,
+                                          const float* sum, float scale, int accumulate) {
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    Grad* row = dtable + v * ld;
+    if (accumulate) load_cols<Grad, VECTOR>(row, c0, lane, H, o);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = fmaf(sum[i], scale, o[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = sum[i] * scale;
-    }
-    store8<Grad, VECTOR>(dst, n, o);
+    for (int i = 0; i < 8; ++i) o[i] = accumulate ? fmaf(sum[i], scale, o[i]) : sum[i] * scale;
+    store_cols<Grad, VECTOR>(row, c0, lane, H, o);
 }
 
 // FP32 partial rows: two per range, [0] a run that began before the range, [1] a run that
-// goes on after it.  Rows are Hp columns (H rounded up to 8), 32-byte aligned.
-__device__ __forceinline__ float* partial_row(float* part, int range, int which, int64_t Hp) {
-    return part + ((int64_t)range * 2 + which) * Hp;
+// goes on after it.  Rows are Hp columns (H rounded up to 8).
+__device__ __forceinline__ float* partial_row(float* part, int64_t range, int which, int64_t Hp) {
+    return part + (range * 2 + which) * Hp;
 }
 
-// One warp per (range of kEmbedRange places, 256 columns).
-template <typename In, typename Grad, bool VEC_IN, bool VEC_OUT>
-__global__ void __launch_bounds__(128)
-    embed_segment_kernel(const int32_t* __restrict__ order, const int32_t* __restrict__ key,
-                         const int32_t* __restrict__ n_live, const In* __restrict__ dout, int64_t ld_dout, int64_t H,
-                         float scale, Grad* dtable, int64_t ld, int accumulate, float* __restrict__ part,
-                         int ranges, int chunks) {
+struct EmbedSumArgs {
+    const int32_t* order;
+    const int32_t* key;
+    const int32_t* n_live;
+    const void* dout;
+    int64_t ld_dout, H;
+    float scale;
+    void* dtable;
+    int64_t ld;
+    int accumulate;
+    float* part;
+    int places;               // sorted tokens per range
+    int ranges, chunks;
+};
+
+constexpr int kSumWarps = 4;
+constexpr int kFillThreads = 256;
+constexpr int kFillBytes = 16384;             // about what one CTA fills
+
+// Sets one row to zero, thread `t` of `threads`: 16-byte stores, single elements at the ends of
+// an unaligned row.
+template <typename Grad>
+__device__ __forceinline__ void zero_row(Grad* row, int64_t H, int t, int threads) {
+    constexpr int VEC = 16 / sizeof(Grad);
+    int64_t head = (VEC - (int64_t)((uintptr_t)row / sizeof(Grad) % VEC)) % VEC;
+    if (head > H) head = H;
+    const int vectors = (int)((H - head) / VEC);
+    Grad* body = row + head;
+#pragma unroll 4
+    for (int i = t; i < vectors; i += threads) st_v4(body + (int64_t)i * VEC, make_uint4(0u, 0u, 0u, 0u));
+    if (t < head) row[t] = Grad(0);
+    if (t < H - head - (int64_t)vectors * VEC) body[(int64_t)vectors * VEC + t] = Grad(0);
+}
+
+// Sets the rows without a token to zero: long rows one per CTA, short ones (at most half of
+// kFillBytes) one per warp, fill_rows per CTA.  Many short CTAs in address order rather than a
+// few that stride over the table: 7.8 against 6.6 TB/s on 3.7 GB, as the DRAM sees one moving
+// front of writes.  A kernel of its own, because it needs every thread an SM can hold to cover
+// the look at `present`.
+template <typename Grad>
+__global__ void __launch_bounds__(kFillThreads)
+    embed_fill_kernel(const uint32_t* __restrict__ present, int64_t V, int64_t H, Grad* __restrict__ dtable,
+                      int64_t ld, int fill_rows) {
+    grid_dependency_wait();
+    if (fill_rows == 1) {
+        const uint32_t v = blockIdx.x;
+        if (!(present[v / 32] >> (v % 32) & 1)) zero_row(dtable + (int64_t)v * ld, H, threadIdx.x, kFillThreads);
+        return;
+    }
+    const int64_t v0 = (int64_t)blockIdx.x * fill_rows;
+    for (int i = threadIdx.x / 32; i < fill_rows && v0 + i < V; i += kFillThreads / 32) {
+        const int64_t v = v0 + i;
+        if (!(present[v / 32] >> (v % 32) & 1)) zero_row(dtable + v * ld, H, threadIdx.x % 32, 32);
+    }
+}
+
+// Launches a kernel that waits on the device for the one before it in the stream, so that its
+// launch overlaps that one's end.
+template <typename... Params, typename... Args>
+static cudaError_t launch_after(void (*k)(Params...), int64_t blocks, int threads, cudaStream_t stream,
+                                const Args&... args) {
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = stream;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
+template <typename Grad>
+static cudaError_t launch_fill_t(const EmbedBackward& c, cudaStream_t stream) {
+    const int64_t row_bytes = c.H * (int64_t)sizeof(Grad);
+    const int fill_rows = row_bytes > kFillBytes / 2 ? 1 : (int)(kFillBytes / row_bytes);
+    const int64_t blocks = (c.V + fill_rows - 1) / fill_rows;
+    return launch_after(embed_fill_kernel<Grad>, blocks, kFillThreads, stream, (const uint32_t*)c.present, c.V, c.H,
+                        (Grad*)c.dtable, c.ld_dtable, fill_rows);
+}
+
+// One warp per (range of places, 256 columns).
+template <typename In, typename Grad, bool VECTOR>
+__global__ void __launch_bounds__(kSumWarps * 32) embed_segment_kernel(const __grid_constant__ EmbedSumArgs a) {
+    grid_dependency_wait();
     const int lane = threadIdx.x % 32;
-    const int64_t item = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
-    if (item >= (int64_t)ranges * chunks) return;
-    const int range = (int)(item / chunks);
-    const int64_t c = (item % chunks) * 256 + lane * 8;
-    const int live = *n_live;
-    const int p0 = range * kEmbedRange;
+    const int64_t item = (int64_t)blockIdx.x * kSumWarps + threadIdx.x / 32;
+    if (item >= (int64_t)a.ranges * a.chunks) return;
+    const int range = (int)(item / a.chunks);
+    const int64_t c0 = (item - (int64_t)range * a.chunks) * 256;
+    const int live = *a.n_live;
+    const int p0 = range * a.places;
     if (p0 >= live) return;
-    const int cnt = min(kEmbedRange, live - p0);
-    const int my_key = lane < cnt ? key[p0 + lane] : -1;
-    const int my_pos = lane < cnt ? order[p0 + lane] : 0;
-    const int before = p0 ? key[p0 - 1] : -1;
-    const int after = p0 + cnt < live ? key[p0 + cnt] : -1;
-    const int n = c < H ? (int)(H - c < 8 ? H - c : 8) : 0;
-    const int64_t Hp = (H + 7) / 8 * 8;
+    const int cnt = min(a.places, live - p0);
+    const int my_key = lane < cnt ? a.key[p0 + lane] : -1;
+    const int my_pos = lane < cnt ? a.order[p0 + lane] : 0;
+    const int before = p0 ? a.key[p0 - 1] : -1;
+    const int after = p0 + cnt < live ? a.key[p0 + cnt] : -1;
+    const int64_t Hp = (a.H + 7) / 8 * 8;
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     bool from_before = __shfl_sync(0xffffffffu, my_key, 0) == before;
-    constexpr int U = 8;
+    constexpr int U = RawCols<In, VECTOR>::kPacked ? 8 : 4;
     for (int i0 = 0; i0 < cnt; i0 += U) {
-        float v[U][8];
+        RawCols<In, VECTOR> v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t pos = __shfl_sync(0xffffffffu, my_pos, (i0 + u) & 31);
-            if (i0 + u < cnt && n > 0) load8<In, VEC_IN>(dout + pos * ld_dout + c, n, v[u]);
+            if (i0 + u < cnt) v[u].load((const In*)a.dout + pos * a.ld_dout, c0, lane, a.H);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = i0 + u;
             const int k = __shfl_sync(0xffffffffu, my_key, i & 31);
-            const int k_next = i + 1 < cnt ? __shfl_sync(0xffffffffu, my_key, (i + 1) & 31) : after;
+            const int k_in = __shfl_sync(0xffffffffu, my_key, (i + 1) & 31);
             if (i < cnt) {
-                if (n > 0)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) sum[j] += v[u][j];
+                const int k_next = i + 1 < cnt ? k_in : after;
+                v[u].add_to(sum);
                 if (k != k_next || i + 1 == cnt) {
-                    if (n > 0) {
-                        if (from_before) store8<float, true>(partial_row(part, range, 0, Hp) + c, 8, sum);
-                        else if (k == k_next) store8<float, true>(partial_row(part, range, 1, Hp) + c, 8, sum);
-                        else write_row<Grad, VEC_OUT>(dtable, ld, k, c, n, sum, scale, accumulate);
-                    }
+                    if (from_before)
+                        store_cols<float, VECTOR>(partial_row(a.part, range, 0, Hp), c0, lane, a.H, sum);
+                    else if (k == k_next)
+                        store_cols<float, VECTOR>(partial_row(a.part, range, 1, Hp), c0, lane, a.H, sum);
+                    else
+                        write_row<Grad, VECTOR>((Grad*)a.dtable, a.ld, k, c0, lane, a.H, sum, a.scale, a.accumulate);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) sum[j] = 0.f;
                     from_before = false;
@@ -306,83 +474,100 @@ __global__ void __launch_bounds__(128)
 
 // One warp per (range, 256 columns): if the range's last run begins in it and goes on, the
 // run's partial rows are added in order and written.
-template <typename Grad, bool VEC_OUT>
-__global__ void __launch_bounds__(128)
-    embed_join_kernel(const int32_t* __restrict__ key, const int32_t* __restrict__ n_live, int64_t H, float scale,
-                      Grad* dtable, int64_t ld, int accumulate, float* part, int ranges, int chunks) {
+template <typename Grad, bool VECTOR>
+__global__ void __launch_bounds__(kSumWarps * 32) embed_join_kernel(const __grid_constant__ EmbedSumArgs a) {
+    grid_dependency_wait();
     const int lane = threadIdx.x % 32;
-    const int64_t item = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
-    if (item >= (int64_t)ranges * chunks) return;
-    const int range = (int)(item / chunks);
-    const int live = *n_live;
-    const int p0 = range * kEmbedRange, p1 = p0 + kEmbedRange;
+    const int64_t item = (int64_t)blockIdx.x * kSumWarps + threadIdx.x / 32;
+    if (item >= (int64_t)a.ranges * a.chunks) return;
+    const int range = (int)(item / a.chunks);
+    const int live = *a.n_live;
+    const int p0 = range * a.places, p1 = p0 + a.places;
     if (p1 >= live) return;                                       // nothing follows this range
-    const int k = key[p1 - 1];
-    if (key[p1] != k) return;                                     // the last run ends here
-    if (key[p0] == k && p0 > 0 && key[p0 - 1] == k) return;       // it began in an earlier range
-    const int64_t c = (item % chunks) * 256 + lane * 8;
-    if (c >= H) return;
-    const int64_t Hp = (H + 7) / 8 * 8;
-    float sum[8], v[8];
-    load8<float, true>(partial_row(part, range, 1, Hp) + c, 8, sum);
-    for (int r = range + 1;; ++r) {
-        load8<float, true>(partial_row(part, r, 0, Hp) + c, 8, v);
+    const int k = a.key[p1 - 1];
+    if (a.key[p1] != k) return;                                   // the last run ends here
+    if (a.key[p0] == k && p0 > 0 && a.key[p0 - 1] == k) return;   // it began in an earlier range
+    const int64_t c0 = (item - (int64_t)range * a.chunks) * 256;
+    const int64_t Hp = (a.H + 7) / 8 * 8;
+    float sum[8];
+    load_cols<float, VECTOR>(partial_row(a.part, range, 1, Hp), c0, lane, a.H, sum);
+    for (int r0 = range + 1;; r0 += 32) {
+        // equal ids are neighbours: the run covers the next ranges as long as they begin with it
+        const int64_t first = (int64_t)(r0 + lane) * a.places;
+        const unsigned in = __ballot_sync(0xffffffffu, first < live && a.key[first] == k);
+        const int n = in == 0xffffffffu ? 32 : __ffs(~in) - 1;
+        constexpr int U = 8;
+        for (int i0 = 0; i0 < n; i0 += U) {
+            float v[U][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] += v[j];
-        const int end = (r + 1) * kEmbedRange;
-        if (end >= live || key[end] != k) break;                  // equal ids are neighbours
+            for (int u = 0; u < U; ++u)
+                if (i0 + u < n)
+                    load_cols<float, VECTOR>(partial_row(a.part, r0 + i0 + u, 0, Hp), c0, lane, a.H, v[u]);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i0 + u < n) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[j] += v[u][j];
+                }
+        }
+        if (n < 32) break;
     }
-    write_row<Grad, VEC_OUT>(dtable, ld, k, c, (int)(H - c < 8 ? H - c : 8), sum, scale, accumulate);
+    write_row<Grad, VECTOR>((Grad*)a.dtable, a.ld, k, c0, lane, a.H, sum, a.scale, a.accumulate);
 }
 
 // ------------------------------------------------------------------------ host side
-template <typename Id, typename Grad>
-static cudaError_t launch_order_t(const EmbedBackward& c, bool vec, cudaStream_t stream) {
-    int64_t grid = c.num_sms;
-    if (grid > c.V) grid = c.V;
-    const int64_t widest = 8192;                                  // ids per CTA: 32 KB of counters
-    if ((c.V + grid - 1) / grid > widest) grid = (c.V + widest - 1) / widest;
-    const int range = (int)((c.V + grid - 1) / grid);
-    grid = (c.V + range - 1) / range;
-    auto* k = vec ? embed_order_kernel<Id, Grad, true> : embed_order_kernel<Id, Grad, false>;
-    k<<<(unsigned)grid, kOrderThreads, (size_t)range * sizeof(int), stream>>>(
-        (const Id*)c.ids, (int)c.N, c.V, range, c.order, c.key, c.n_live, (Grad*)c.dtable, c.H, c.ld_dtable,
-        !c.accumulate, c.ws);
+template <typename Id>
+static cudaError_t launch_order_t(const EmbedBackward& c, cudaStream_t stream) {
+    // one CTA per SM, ranges of whole words of `present` and at most 2048 ids (8 KB of counters
+    // beside the 32 KB list)
+    int64_t range = (c.V + c.num_sms - 1) / c.num_sms;
+    range = (range + 31) / 32 * 32;
+    if (range > 2048) range = 2048;
+    const int64_t grid = (c.V + range - 1) / range;
+    embed_order_kernel<Id><<<(unsigned)grid, kOrderThreads, (size_t)range * sizeof(int), stream>>>(
+        (const Id*)c.ids, (int)c.N, c.V, (int)range, c.order, c.key, c.n_live, c.present, c.ws);
     return cudaGetLastError();
 }
 
 template <typename In, typename Grad>
-static cudaError_t launch_sums_t(const EmbedBackward& c, bool vec_out, cudaStream_t stream) {
-    const bool vec_in = rows_in_groups(c.dout, c.H, c.ld_dout, c.dout_dtype);
-    const int ranges = embed_ranges(c.N);
-    const int64_t chunks = (c.H + 255) / 256;
-    const int64_t blocks = (ranges * chunks + 3) / 4;
+static cudaError_t launch_sums_t(const EmbedBackward& c, cudaStream_t stream) {
+    const bool vec = rows_in_groups(c.dout, c.H, c.ld_dout, c.dout_dtype) &&
+                     rows_in_groups(c.dtable, c.H, c.ld_dtable, c.dtable_dtype);
+    EmbedSumArgs a{};
+    a.order = c.order;
+    a.key = c.key;
+    a.n_live = c.n_live;
+    a.dout = c.dout;
+    a.ld_dout = c.ld_dout;
+    a.H = c.H;
+    a.scale = c.scale;
+    a.dtable = c.dtable;
+    a.ld = c.ld_dtable;
+    a.accumulate = c.accumulate;
+    a.part = c.part;
+    a.places = embed_places(c.N, c.H);
+    a.ranges = embed_ranges(c.N, c.H);
+    a.chunks = (int)((c.H + 255) / 256);
+    const int64_t blocks = ((int64_t)a.ranges * a.chunks + kSumWarps - 1) / kSumWarps;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    auto* k = vec_in ? (vec_out ? embed_segment_kernel<In, Grad, true, true> : embed_segment_kernel<In, Grad, true, false>)
-                     : (vec_out ? embed_segment_kernel<In, Grad, false, true> : embed_segment_kernel<In, Grad, false, false>);
-    k<<<(unsigned)blocks, 128, 0, stream>>>(c.order, c.key, c.n_live, (const In*)c.dout, c.ld_dout, c.H, c.scale,
-                                            (Grad*)c.dtable, c.ld_dtable, c.accumulate, c.part, ranges, (int)chunks);
-    cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess || ranges == 1) return err;            // one range: no run crosses
-    auto* j = vec_out ? embed_join_kernel<Grad, true> : embed_join_kernel<Grad, false>;
-    j<<<(unsigned)blocks, 128, 0, stream>>>(c.key, c.n_live, c.H, c.scale, (Grad*)c.dtable, c.ld_dtable, c.accumulate,
-                                            c.part, ranges, (int)chunks);
-    return cudaGetLastError();
+    if (blocks == 0) return cudaSuccess;
+    auto* k = vec ? embed_segment_kernel<In, Grad, true> : embed_segment_kernel<In, Grad, false>;
+    cudaError_t err = launch_after(k, blocks, kSumWarps * 32, stream, a);
+    if (err != cudaSuccess || a.ranges <= 1) return err;          // one range: no run crosses
+    auto* j = vec ? embed_join_kernel<Grad, true> : embed_join_kernel<Grad, false>;
+    return launch_after(j, blocks, kSumWarps * 32, stream, a);
 }
 
 cudaError_t launch_embedding_backward(const EmbedBackward& c, cudaStream_t stream) {
-    const bool vec_out = rows_in_groups(c.dtable, c.H, c.ld_dtable, c.dtable_dtype);
-    const bool f32 = c.dtable_dtype == MOE_F32;
-    cudaError_t err = c.id_bytes == 8
-                          ? (f32 ? launch_order_t<int64_t, float>(c, vec_out, stream)
-                                 : launch_order_t<int64_t, uint16_t>(c, vec_out, stream))
-                          : (f32 ? launch_order_t<int32_t, float>(c, vec_out, stream)
-                                 : launch_order_t<int32_t, uint16_t>(c, vec_out, stream));
-    if (err != cudaSuccess || c.N == 0) return err;
+    cudaError_t err = c.id_bytes == 8 ? launch_order_t<int64_t>(c, stream) : launch_order_t<int32_t>(c, stream);
+    if (err == cudaSuccess && !c.accumulate)
+        err = c.dtable_dtype == MOE_F32 ? launch_fill_t<float>(c, stream) : launch_fill_t<uint16_t>(c, stream);
+    if (err != cudaSuccess) return err;
     if (c.dout_dtype == MOE_F32)
-        return f32 ? launch_sums_t<float, float>(c, vec_out, stream) : launch_sums_t<float, uint16_t>(c, vec_out, stream);
-    return f32 ? launch_sums_t<uint16_t, float>(c, vec_out, stream)
-               : launch_sums_t<uint16_t, uint16_t>(c, vec_out, stream);
+        return c.dtable_dtype == MOE_F32 ? launch_sums_t<float, float>(c, stream)
+                                         : launch_sums_t<float, uint16_t>(c, stream);
+    return c.dtable_dtype == MOE_F32 ? launch_sums_t<uint16_t, float>(c, stream)
+                                     : launch_sums_t<uint16_t, uint16_t>(c, stream);
 }
 
 }  // namespace moe

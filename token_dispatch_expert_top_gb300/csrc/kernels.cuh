@@ -208,9 +208,18 @@ bool encode_ffn_maps(const TcFfnCall& c, FfnMaps* m, GemmSide* s1, GemmSide* s2)
 // Token embedding and its gradient (embedding.cu).
 cudaError_t launch_embedding(const void* ids, int id_bytes, int64_t N, const void* table, int table_dtype, int64_t V,
                              int64_t H, int64_t ld_table, float scale, void* out, int out_dtype, int64_t ld_out,
-                             int num_sms, WsHeader* ws, cudaStream_t stream);
-constexpr int kEmbedRange = 32;    // sorted tokens per range of the gradient's sums (one per lane)
-inline int embed_ranges(int64_t N) { return (int)((N + kEmbedRange - 1) / kEmbedRange); }
+                             WsHeader* ws, cudaStream_t stream);
+// Sorted tokens per range of the gradient's sums: 32 (one per lane) where that gives work to
+// 2048 warps (one per 256 columns of a range), fewer down to 4 for short batches.
+inline int embed_places(int64_t N, int64_t H) {
+    int places = 32;
+    while (places > 4 && (N + places - 1) / places * ((H + 255) / 256) < 2048) places /= 2;
+    return places;
+}
+inline int embed_ranges(int64_t N, int64_t H) {
+    const int places = embed_places(N, H);
+    return (int)((N + places - 1) / places);
+}
 struct EmbedBackward {
     const void* ids;
     int id_bytes;
@@ -226,6 +235,7 @@ struct EmbedBackward {
     int32_t* order;           // [N] scratch: tokens sorted by (id, token)
     int32_t* key;             // [N] scratch: their ids
     int32_t* n_live;          // [1] scratch: how many have an id
+    uint32_t* present;        // [V / 32, rounded up] scratch: ids that a token names
     float* part;              // [2 ranges][H rounded up to 8] scratch
     int num_sms;
     WsHeader* ws;
@@ -269,7 +279,7 @@ cudaError_t launch_token_logprobs_backward(const LogprobGradCall& c, cudaStream_
 // drops everything.
 cudaError_t launch_dropout(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld_x, const void* residual,
                            int64_t ld_res, uint32_t thr, uint64_t seed, uint64_t offset, void* out, int64_t ld_out,
-                           int num_sms, cudaStream_t stream);
+                           cudaStream_t stream);
 
 // Shape validation shared by the entry points (api.cu): MOE_OK or the status to
 // return before anything is launched.

@@ -15,7 +15,7 @@
 
 namespace moe {
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
@@ -23,34 +23,52 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
-// The same with subnormal results: the gradient multiplies small probabilities by what may
-// be large.
-__device__ __forceinline__ float exp2_full(float x) {
-    float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
+// Two FP32 values in one 64-bit register: one instruction adds or multiplies both.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void f2_split(F2 x, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v));
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
 }
 
-// Running maximum, sum and first moment of a row's exponentials, relative to m:
-// s = sum exp(c d), t = sum d exp(c d), d = x - m.  m starts at the lowest finite value,
-// so masked logits give d = -inf, exp 0.
+// Running sums of a row relative to its largest logit so far, m: with y = (x - m) c2,
+// c2 = scale log2 e, s = sum 2^y, t = sum y 2^y.  Logits are raised to kFloor first: a masked
+// logit then adds 0 to both sums.  Good for rows whose maximum lies inside (-2^59, 2^59) and
+// scales in [2^-20, 2^20]; the careful sums below take the others.
+constexpr float kFloor = -0x1p60f, kFastMax = 0x1p59f;
+constexpr uint32_t kFloorBf16x2 = 0xDD80DD80u;
+inline bool fast_scale(float scale) { return scale >= 0x1p-20f && scale <= 0x1p20f; }
 struct RowSums {
     float m, s, t;
     __device__ void init() {
-        m = -FLT_MAX;
+        m = kFloor;
         s = t = 0.f;
     }
-    // moves the reference point up to m2 >= m
     __device__ void raise(float m2, float c2) {
-        const float d = m - m2, f = exp2_approx(d * c2);
-        t = f > 0.f ? f * fmaf(d, s, t) : 0.f;       // f = 0 may meet d = -inf
+        const float d = (m - m2) * c2, f = exp2_approx(d);
+        t = f * fmaf(d, s, t);
         s *= f;
         m = m2;
-    }
-    __device__ void add(float x, float c2) {
-        const float d = x - m, e = exp2_approx(d * c2);
-        s += e;
-        t = fmaf(e, fmaxf(d, -FLT_MAX), t);          // a masked logit's 0 * -inf is 0
     }
     __device__ void merge(RowSums o, float c2) {
         if (o.m > m) raise(o.m, c2);
@@ -60,24 +78,51 @@ struct RowSums {
     }
 };
 
+// The same for any row and scale: s = sum exp(c d), t = sum d exp(c d),
+// d = x - m.  m starts at the lowest finite value, so masked logits give d = -inf, exp 0.
+struct CarefulSums {
+    float m, s, t;
+    __device__ void init() {
+        m = -FLT_MAX;
+        s = t = 0.f;
+    }
+    __device__ void raise(float m2, float c2) {
+        const float d = m - m2, f = exp2_approx(d * c2);
+        t = f > 0.f ? f * fmaf(d, s, t) : 0.f;       // f = 0 may meet d = -inf
+        s *= f;
+        m = m2;
+    }
+    __device__ void add(float x, float c2) {
+        if (x > m) raise(x, c2);
+        const float d = x - m, e = exp2_approx(d * c2);
+        s += e;
+        t = fmaf(e, fmaxf(d, -FLT_MAX), t);          // a masked logit's 0 * -inf is 0
+    }
+    __device__ void merge(CarefulSums o, float c2) {
+        if (o.m > m) raise(o.m, c2);
+        else o.raise(m, c2);
+        s += o.s;
+        t += o.t;
+    }
+};
+
 // A row as 16-byte vectors of its own alignment: vector v holds the elements
-// v*VEC - mis .. v*VEC - mis + VEC - 1; the first and the last may be partial.
+// v*VEC - mis .. v*VEC - mis + VEC - 1; the first and the last may be partial.  (A row has at
+// most 2^22 elements.)
 template <typename T>
 struct RowView {
     static constexpr int VEC = 16 / sizeof(T);
     const T* p;
-    int64_t V;
-    int mis;
-    int nvec;
-    __device__ RowView(const T* row, int64_t V_) : p(row), V(V_) {
+    int V, mis, nvec;
+    __device__ RowView(const T* row, int V_) : p(row), V(V_) {
         mis = (int)(((uintptr_t)row / sizeof(T)) % VEC);
-        nvec = (int)((V + mis + VEC - 1) / VEC);
+        nvec = (V + mis + VEC - 1) / VEC;
     }
-    __device__ int64_t first(int v) const { return (int64_t)v * VEC - mis; }
-    __device__ bool whole(int v) const { return v >= (mis ? 1 : 0) && first(v) + VEC <= V; }
+    __device__ int first(int v) const { return v * VEC - mis; }
+    __device__ bool whole(int v) const { return first(v) >= 0 && first(v) + VEC <= V; }
     // the vector's elements; fill past the row
     __device__ uint4 load(int v, float fill) const {
-        const int64_t j = first(v);
+        const int j = first(v);
         if (whole(v)) return ld_nc_v4(p + j);
         T e[VEC];
 #pragma unroll
@@ -111,38 +156,55 @@ __device__ __forceinline__ float value_of(uint32_t o) {
     return o == 0u ? __uint_as_float(0x7FC00000u) : __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
 }
 
-// The best entry over the warp by (key descending, index ascending); every lane gets it.
-__device__ __forceinline__ void warp_best(uint32_t key, uint32_t idx, uint32_t* best_key, uint32_t* best_idx) {
-    *best_key = __reduce_max_sync(0xffffffffu, key);
-    *best_idx = __reduce_min_sync(0xffffffffu, key == *best_key ? idx : 0xFFFFFFFFu);
-}
+// An entry as one number: the larger one is the better one.
+__device__ __forceinline__ uint64_t pack_entry(uint32_t key, uint32_t idx) { return (uint64_t)key << 32 | (uint32_t)~idx; }
 
-// A warp's sorted list, entry i in lane i.  Inserts (k, j) if it beats entry n-1.
+// A warp's list of entries (key, idx), best first (key descending, then idx ascending), entry
+// i in lane i; empty entries are (0, kNone).
+constexpr uint32_t kNone = 0xFFFFFFFFu;
 struct WarpList {
     uint32_t key, idx;
-    __device__ void init() { key = 0, idx = 0xFFFFFFFFu; }
+    __device__ void init() { key = 0u, idx = kNone; }
     __device__ static bool beats(uint32_t k, uint32_t j, uint32_t k2, uint32_t j2) {
         return k > k2 || (k == k2 && j < j2);
     }
-    __device__ void insert(uint32_t k, uint32_t j) {
+    // Compares with the entry `stride` lanes away and keeps the better one where `first`.
+    __device__ void exchange(int stride, bool first) {
+        const uint32_t k = __shfl_xor_sync(0xffffffffu, key, stride), j = __shfl_xor_sync(0xffffffffu, idx, stride);
+        if (beats(k, j, key, idx) == first && (k != key || j != idx)) key = k, idx = j;
+    }
+    // Bitonic sort of any 32 entries.
+    __device__ void sort() {
         const int lane = threadIdx.x % 32;
-        const unsigned after = __ballot_sync(0xffffffffu, beats(k, j, key, idx));   // entries that move down
-        const uint32_t up_key = __shfl_up_sync(0xffffffffu, key, 1), up_idx = __shfl_up_sync(0xffffffffu, idx, 1);
-        if (after >> lane & 1) {
-            const bool here = lane == __ffs(after) - 1;
-            key = here ? k : up_key;
-            idx = here ? j : up_idx;
-        }
+#pragma unroll
+        for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+            for (int stride = size / 2; stride; stride /= 2)
+                exchange(stride, ((lane & stride) == 0) == ((lane & size) == 0));
+    }
+    // The best 32 of this list and another sorted one, whose entry 31 - lane is (k, j).
+    __device__ void merge_reversed(uint32_t k, uint32_t j) {
+        const int lane = threadIdx.x % 32;
+        if (beats(k, j, key, idx)) key = k, idx = j;
+#pragma unroll
+        for (int stride = 16; stride; stride /= 2) exchange(stride, (lane & stride) == 0);
     }
 };
 
-constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
-constexpr int kLpUnroll = 4;
+constexpr int kLpMaxWarps = 32;
+constexpr int kLpUnroll = 4;                    // vectors a lane holds at once
+constexpr int kLpChunk = 32 * kLpUnroll;        // vectors a warp reads at once: one chunk
+constexpr int kLpMaxCluster = 8;
+constexpr int kLpRanked = 256;                  // chunks that are ranked by all comparisons
+constexpr int kLpCandidates = 256;              // logits that are
+static_assert(kLpMaxCluster * kMaxTop <= kLpCandidates, "the CTAs' lists are ranked together");
 
 struct LogprobArgs {
     const void* logits;
-    int64_t V, ld;
+    int V;
+    int64_t ld;
     float scale;
+    int careful;                                // the scale is outside the fast sums' range
     const void* targets;
     float *logp, *entropy, *stats;
     int n_top;
@@ -151,51 +213,144 @@ struct LogprobArgs {
     WsHeader* ws;
 };
 
-// One CTA per row, one pass over it.  For the top list the pass only keeps the maximum of
-// each chunk of 32 vectors (what a warp reads at once).  The n best logits lie in the n best
-// chunks by (maximum, position): a chunk below those has n chunks before it, each with a
-// logit that beats all of its own.  So n chunks are read again, from L2, whatever the
-// logits are.
-template <typename T, typename Id>
-__global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const __grid_constant__ LogprobArgs a) {
-    extern __shared__ uint32_t chunk_max[];                  // order_of the chunk's maximum; 0: taken
-    __shared__ RowSums warp_sums[kLpWarps];
-    __shared__ uint32_t sel[kMaxTop];
-    __shared__ uint32_t list_key[kLpWarps][kMaxTop], list_idx[kLpWarps][kMaxTop];
-    constexpr int VEC = RowView<T>::VEC;
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int64_t r = blockIdx.x;
-    const RowView<T> row((const T*)a.logits + r * a.ld, a.V);
-    const int chunks = (row.nvec + 31) / 32;
-    const float c2 = a.scale * kLog2e;
-    RowSums sums;
-    sums.init();
-    for (int g0 = warp; g0 < chunks; g0 += kLpWarps * kLpUnroll) {
-        uint4 q[kLpUnroll];
-#pragma unroll
-        for (int u = 0; u < kLpUnroll; ++u) {
-            const int v = (g0 + u * kLpWarps) * 32 + lane;
-            const uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;      // -inf
-            q[u] = v < row.nvec ? row.load(v, -INFINITY) : make_uint4(none, none, none, none);
-        }
-        float x[kLpUnroll][VEC], top = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < kLpUnroll; ++u) {
-            RowView<T>::unpack(q[u], x[u]);
-            float mx = x[u][0];
-#pragma unroll
-            for (int i = 1; i < VEC; ++i) mx = fmaxf(mx, x[u][i]);
-            top = fmaxf(top, mx);
-            if (a.n_top) {
-                const uint32_t o = __reduce_max_sync(0xffffffffu, max(order_of(mx), 1u));
-                if (lane == 0 && g0 + u * kLpWarps < chunks) chunk_max[g0 + u * kLpWarps] = o;
-            }
-        }
-        if (top > sums.m) sums.raise(top, c2);
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Raises both halves to kFloor; NaN stays NaN.
+__device__ __forceinline__ uint32_t floor_bf16x2(uint32_t a) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(kFloorBf16x2));
+    return r;
+}
+__device__ __forceinline__ float floor_f32(float a) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(kFloor));
+    return r;
+}
+
+// A float in the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ float ld_cluster_f32(const void* p, uint32_t rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(p), rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint64_t ld_cluster_u64(const void* p, uint32_t rank) {
+    uint64_t v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(mapa_shared(smem_u32(p), rank)) : "memory");
+    return v;
+}
+
+// Largest logit of the lane's vectors (NaN ignored).
+template <typename T>
+__device__ __forceinline__ float lane_max(const uint4 (&q)[kLpUnroll]) {
+    if constexpr (sizeof(T) == 2) {
+        uint32_t h = 0xFF80FF80u;               // -inf, -inf
 #pragma unroll
         for (int u = 0; u < kLpUnroll; ++u)
+            h = max_bf16x2(h, max_bf16x2(max_bf16x2(q[u].x, q[u].y), max_bf16x2(q[u].z, q[u].w)));
+        return fmaxf(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u));
+    } else {
+        float h = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) sums.add(x[u][i], c2);
+        for (int u = 0; u < kLpUnroll; ++u)
+            h = fmaxf(h, fmaxf(fmaxf(__uint_as_float(q[u].x), __uint_as_float(q[u].y)),
+                               fmaxf(__uint_as_float(q[u].z), __uint_as_float(q[u].w))));
+        return h;
+    }
+}
+
+// Adds 2^y and y 2^y of the lane's vectors.
+template <typename T>
+__device__ __forceinline__ void add_vectors(const uint4 (&q)[kLpUnroll], float c2, RowSums& sums) {
+    const F2 c = f2(c2, c2), r = f2(-sums.m, -sums.m);
+    F2 s[2] = {f2(sums.s, 0.f), f2(0.f, 0.f)}, t[2] = {f2(sums.t, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+    for (int u = 0; u < kLpUnroll; ++u) {
+        const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+        constexpr int P = sizeof(T) == 2 ? 4 : 2;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            F2 x;
+            if constexpr (sizeof(T) == 2) {
+                const uint32_t h = floor_bf16x2(w[p]);
+                x = f2(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u));
+            } else {
+                x = f2(floor_f32(__uint_as_float(w[2 * p])), floor_f32(__uint_as_float(w[2 * p + 1])));
+            }
+            const F2 y = f2_mul(f2_add(x, r), c);
+            float y0, y1;
+            f2_split(y, y0, y1);
+            const F2 e = f2(exp2_approx(y0), exp2_approx(y1));
+            s[p & 1] = f2_add(s[p & 1], e);
+            t[p & 1] = f2_fma(e, y, t[p & 1]);
+        }
+    }
+    float a, b;
+    f2_split(f2_add(s[0], s[1]), a, b);
+    sums.s = a + b;
+    f2_split(f2_add(t[0], t[1]), a, b);
+    sums.t = a + b;
+}
+
+// One cluster of CTAs per row (each takes a contiguous share of the row's chunks), one pass
+// over the row.  Bound by HBM: 8 loads of 16 bytes per lane are in flight at most, 32 warps
+// an SM; per BF16 logit about 5 instructions are issued, of which one is the exponential.
+// For the top list the pass only keeps the maximum of each chunk (kLpChunk vectors: what a
+// warp reads at once).  The n best logits lie in the n best chunks by (maximum, position): a
+// chunk below those has n chunks before it, each with a logit that beats all of its own.  So
+// n chunks are read again, from L2, and of them only the logits that reach the n-th best
+// maximum matter.  Those are few; where ties and masks make them many, the same argument
+// picks the n best vectors of the n chunks, which are 8 n (FP32: 4 n) logits to sort.
+template <typename T, typename Id, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) logprobs_kernel(const __grid_constant__ LogprobArgs a) {
+    extern __shared__ __align__(16) uint32_t chunk_max[];    // order_of the chunk's maximum, at least 1; four zeros
+    __shared__ RowSums warp_sums[WARPS], cta_sums;
+    __shared__ CarefulSums warp_careful[WARPS], cta_careful;
+    __shared__ uint32_t sel[32], least;
+    __shared__ uint32_t list_key[WARPS][32], list_idx[WARPS][32];
+    __shared__ uint64_t candidates[kLpCandidates], cta_list[32];
+    __shared__ int found;
+    constexpr int VEC = RowView<T>::VEC;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+    const uint32_t rank = cluster_ctarank(), ctas = cluster_nctarank();
+    const int64_t r = blockIdx.x / ctas;
+    const RowView<T> row((const T*)a.logits + r * a.ld, a.V);
+    const int row_chunks = (row.nvec + kLpChunk - 1) / kLpChunk;
+    const int share = (row_chunks + (int)ctas - 1) / (int)ctas;
+    const int g_first = (int)rank * share;
+    const int chunks = max(0, min(share, row_chunks - g_first));     // this CTA's
+    const float c2 = a.scale * kLog2e;
+    auto load_chunk = [&](int g, uint4 (&q)[kLpUnroll]) {
+        const int v0 = (g_first + g) * kLpChunk;
+        const T* p = row.p + row.first(v0) + lane * VEC;
+        if (row.whole(v0) && row.whole(v0 + kLpChunk - 1)) {         // the same for the whole warp
+#pragma unroll
+            for (int u = 0; u < kLpUnroll; ++u) q[u] = ld_nc_v4(p + u * 32 * VEC);
+        } else {
+            const uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;      // -inf
+#pragma unroll
+            for (int u = 0; u < kLpUnroll; ++u) {
+                const int v = v0 + u * 32 + lane;
+                q[u] = v < row.nvec ? row.load(v, -INFINITY) : make_uint4(none, none, none, none);
+            }
+        }
+    };
+
+    if (a.n_top && threadIdx.x < 4) chunk_max[chunks + threadIdx.x] = 0u;
+    RowSums sums;
+    sums.init();
+    for (int g = warp; g < chunks; g += warps) {
+        uint4 q[kLpUnroll];
+        load_chunk(g, q);
+        const float top = lane_max<T>(q);
+        if (a.n_top) {
+            const uint32_t o = __reduce_max_sync(0xffffffffu, max(order_of(top), 1u));
+            if (lane == 0) chunk_max[g] = o;
+        }
+        if (top > sums.m) sums.raise(top, c2);
+        add_vectors<T>(q, c2, sums);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -207,12 +362,79 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const __grid_co
     }
     if (lane == 0) warp_sums[warp] = sums;
     __syncthreads();
-    sums = warp_sums[0];
-    for (int w = 1; w < kLpWarps; ++w) sums.merge(warp_sums[w], c2);
-    const bool empty = sums.s == 0.f;
-    const float ls = empty ? -INFINITY : logf(sums.s);
-    auto logp_of = [&](float x) { return empty || x == -INFINITY ? -INFINITY : (x - sums.m) * a.scale - ls; };
-    if (threadIdx.x == 0) {
+    sums.init();
+    if (lane < warps) sums = warp_sums[lane];
+    for (int o = WARPS / 2; o; o >>= 1) {
+        RowSums other;
+        other.m = __shfl_xor_sync(0xffffffffu, sums.m, o);
+        other.s = __shfl_xor_sync(0xffffffffu, sums.s, o);
+        other.t = __shfl_xor_sync(0xffffffffu, sums.t, o);
+        sums.merge(other, c2);
+    }
+    // lane 0's, so that every thread holds the same bits
+    sums.m = __shfl_sync(0xffffffffu, sums.m, 0);
+    sums.s = __shfl_sync(0xffffffffu, sums.s, 0);
+    sums.t = __shfl_sync(0xffffffffu, sums.t, 0);
+    if (ctas > 1) {
+        if (threadIdx.x == 0) cta_sums = sums;
+        cluster_sync();
+        sums.init();
+        for (uint32_t k = 0; k < ctas; ++k) {
+            RowSums o;
+            o.m = ld_cluster_f32(&cta_sums.m, k), o.s = ld_cluster_f32(&cta_sums.s, k);
+            o.t = ld_cluster_f32(&cta_sums.t, k);
+            sums.merge(o, c2);
+        }
+    }
+    float m = sums.m, ls, entropy;
+    if (a.careful || !(fabsf(m) < kFastMax)) {
+        // the same in every CTA of the cluster
+        CarefulSums cs;
+        cs.init();
+        for (int g = warp; g < chunks; g += warps) {
+            uint4 q[kLpUnroll];
+            load_chunk(g, q);
+#pragma unroll
+            for (int u = 0; u < kLpUnroll; ++u) {
+                float x[VEC];
+                RowView<T>::unpack(q[u], x);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) cs.add(x[i], c2);
+            }
+        }
+        for (int o = 16; o; o >>= 1) {
+            CarefulSums other;
+            other.m = __shfl_xor_sync(0xffffffffu, cs.m, o);
+            other.s = __shfl_xor_sync(0xffffffffu, cs.s, o);
+            other.t = __shfl_xor_sync(0xffffffffu, cs.t, o);
+            cs.merge(other, c2);
+        }
+        if (lane == 0) warp_careful[warp] = cs;
+        __syncthreads();
+        cs = warp_careful[0];
+        for (int w = 1; w < warps; ++w) cs.merge(warp_careful[w], c2);
+        if (ctas > 1) {
+            if (threadIdx.x == 0) cta_careful = cs;
+            cluster_sync();
+            cs.init();
+            for (uint32_t k = 0; k < ctas; ++k) {
+                CarefulSums o;
+                o.m = ld_cluster_f32(&cta_careful.m, k), o.s = ld_cluster_f32(&cta_careful.s, k);
+                o.t = ld_cluster_f32(&cta_careful.t, k);
+                cs.merge(o, c2);
+            }
+        }
+        m = cs.m;
+        ls = cs.s == 0.f ? -INFINITY : logf(cs.s);                   // 0: masked throughout
+        entropy = cs.s == 0.f ? 0.f : ls - a.scale * (cs.t / cs.s);
+    } else {
+        const float l2 = log2f(sums.s);
+        ls = kLn2 * l2;
+        entropy = kLn2 * (l2 - sums.t / sums.s);
+    }
+    const bool empty = ls == -INFINITY;
+    auto logp_of = [&](float x) { return empty || x == -INFINITY ? -INFINITY : (x - m) * a.scale - ls; };
+    if (rank == 0 && threadIdx.x == 0) {
         if (a.targets) {
             const Id t = ((const Id*)a.targets)[r];
             float lp = 0.f;
@@ -220,167 +442,360 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const __grid_co
             else if (t >= 0) set_status(a.ws, MOE_ERR_DEVICE_CHECK);
             a.logp[r] = lp;
         }
-        if (a.entropy) a.entropy[r] = empty ? 0.f : ls - a.scale * (sums.t / sums.s);
+        if (a.entropy) a.entropy[r] = entropy;
         if (a.stats) {
-            a.stats[2 * r] = sums.m;
+            a.stats[2 * r] = m;
             a.stats[2 * r + 1] = ls;
         }
     }
-    if (!a.n_top) return;
+    if (!a.n_top) {
+        if (ctas > 1) cluster_sync();                                // remote sums have been read
+        return;
+    }
 
-    // the n best chunks, by one warp: each lane watches every 32nd chunk
-    if (warp == 0) {
-        uint32_t best = 0, at = 0xFFFFFFFFu;
-        auto rescan = [&]() {
-            best = 0, at = 0xFFFFFFFFu;
-            for (int g = lane; g < chunks; g += 32)
-                if (chunk_max[g] > best) best = chunk_max[g], at = g;
-        };
-        rescan();
-        for (int i = 0; i < a.n_top; ++i) {
-            uint32_t k, g;
-            warp_best(best, at, &k, &g);
-            if (lane == 0) sel[i] = g;                       // 0xFFFFFFFF: fewer than n chunks
-            if (g == 0xFFFFFFFFu) continue;
-            if (g % 32 == (uint32_t)lane) {
-                chunk_max[g] = 0;
-                rescan();
+    // Lists of the first `lists` warps -> one list in warp 0.  Every warp calls it; a warp's
+    // place in list_key is written once per call, before the barrier of its level.
+    auto merge_lists = [&](WarpList& list, int lists) {
+        for (int step = 1; step < lists; step *= 2) {
+            if (warp % (2 * step) == step && warp < lists) {
+                list_key[warp][lane] = list.key;
+                list_idx[warp][lane] = list.idx;
             }
+            __syncthreads();
+            if (warp % (2 * step) == 0 && warp + step < lists)
+                list.merge_reversed(list_key[warp + step][31 - lane], list_idx[warp + step][31 - lane]);
         }
-    }
-    __syncthreads();
-    // each warp lists the best of its share of those chunks
-    WarpList list;
-    list.init();
-    for (int i = warp; i < a.n_top; i += kLpWarps) {
-        if (sel[i] == 0xFFFFFFFFu) break;
-        const int v = (int)sel[i] * 32 + lane;
-        float x[VEC];
-        const bool in = v < row.nvec;
-        RowView<T>::unpack(in ? row.load(v, 0.f) : make_uint4(0, 0, 0, 0), x);
+    };
+    // adds an entry per lane to the warp's list, unless none of them beats its n-th
+    auto take = [&](WarpList& list, uint32_t key, uint32_t idx) {
+        const uint32_t last_key = __shfl_sync(0xffffffffu, list.key, a.n_top - 1);
+        const uint32_t last_idx = __shfl_sync(0xffffffffu, list.idx, a.n_top - 1);
+        if (!__any_sync(0xffffffffu, WarpList::beats(key, idx, last_key, last_idx))) return;
+        WarpList next;
+        next.key = key, next.idx = idx;
+        next.sort();
+        list.merge_reversed(__shfl_sync(0xffffffffu, next.key, 31 - lane),
+                            __shfl_sync(0xffffffffu, next.idx, 31 - lane));
+    };
+    const int n = a.n_top;
+    auto write_top = [&](int i, uint32_t key, uint32_t idx) {
+        a.top_idx[r * n + i] = (int32_t)idx;
+        a.top_logp[r * n + i] = logp_of(value_of(key));
+    };
+    // place i of the CTA's own list
+    auto put = [&](int i, uint32_t key, uint32_t idx) {
+        if (ctas > 1) cta_list[i] = pack_entry(key, idx);
+        else write_top(i, key, idx);
+    };
+    bool sorted = true;                                      // by the general way below
+    if (chunks >= n && chunks <= kLpRanked) {
+        // The usual way: every chunk's place by comparing it with all others ...
+        for (int g = threadIdx.x; g < chunks; g += blockDim.x) {
+            const uint32_t key = chunk_max[g];
+            int place = 0;
+#pragma unroll 4
+            for (int o = 0; o < (chunks + 3) / 4; ++o) {     // (the array is zeros up to a multiple of four)
+                const uint4 k = reinterpret_cast<const uint4*>(chunk_max)[o];
+                place += k.x >= key + (4 * o >= g);
+                place += k.y >= key + (4 * o + 1 >= g);
+                place += k.z >= key + (4 * o + 2 >= g);
+                place += k.w >= key + (4 * o + 3 >= g);
+            }
+            if (place < n) sel[place] = g;
+            if (place == n - 1) least = key;                 // no logit below this is needed
+        }
+        if (threadIdx.x == 0) found = 0;
+        __syncthreads();
+        // ... then the logits of the n best that reach the n-th best maximum, in any order ...
+        const uint32_t bound = least;
+        for (int i0 = warp; i0 < n * kLpUnroll; i0 += kLpUnroll * warps) {
+            uint4 q[kLpUnroll];
+            int v[kLpUnroll];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const int64_t j = in ? row.first(v) + e : -1;
-            const uint32_t key = order_of(x[e]);
-            const bool real = j >= 0 && j < a.V;
-            const uint32_t last_key = __shfl_sync(0xffffffffu, list.key, a.n_top - 1);
-            const uint32_t last_idx = __shfl_sync(0xffffffffu, list.idx, a.n_top - 1);
-            unsigned todo = __ballot_sync(0xffffffffu, real && WarpList::beats(key, (uint32_t)j, last_key, last_idx));
-            while (todo) {
-                const int src = __ffs(todo) - 1;
-                todo &= todo - 1;
-                list.insert(__shfl_sync(0xffffffffu, key, src), (uint32_t)__shfl_sync(0xffffffffu, (uint32_t)j, src));
+            for (int u = 0; u < kLpUnroll; ++u) {
+                const int i = i0 + u * warps;
+                v[u] = i < n * kLpUnroll
+                           ? (g_first + (int)sel[i / kLpUnroll]) * kLpChunk + i % kLpUnroll * 32 + lane : row.nvec;
+                if (v[u] < row.nvec) q[u] = row.load(v[u], -INFINITY);
+            }
+#pragma unroll
+            for (int u = 0; u < kLpUnroll; ++u) {
+                if (v[u] >= row.nvec) continue;
+                float x[VEC];
+                RowView<T>::unpack(q[u], x);
+                float mx = x[0];
+#pragma unroll
+                for (int e = 1; e < VEC; ++e) mx = fmaxf(mx, x[e]);
+                if (max(order_of(mx), 1u) < bound) continue;
+                if (*(volatile int*)&found > kLpCandidates) continue;       // too many already
+                const int j0 = row.first(v[u]);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const uint32_t key = order_of(x[e]);
+                    if (j0 + e < 0 || j0 + e >= a.V || max(key, 1u) < bound) continue;
+                    const int at = atomicAdd(&found, 1);
+                    if (at < kLpCandidates) candidates[at] = pack_entry(key, (uint32_t)(j0 + e));
+                }
+            }
+        }
+        __syncthreads();
+        // ... and their places the same way.  Many equal logits: the general way.
+        if (found <= kLpCandidates) {
+            sorted = false;
+            for (int i = threadIdx.x; i < found; i += blockDim.x) {
+                const uint64_t own = candidates[i];
+                int place = 0;
+                for (int o = 0; o < found; ++o) place += candidates[o] > own;
+                if (place < n) put(place, (uint32_t)(own >> 32), ~(uint32_t)own);
             }
         }
     }
-    if (lane < a.n_top) {
-        list_key[warp][lane] = list.key;
-        list_idx[warp][lane] = list.idx;
-    }
-    __syncthreads();
-    // merge the lists: lane w holds warp w's next entry
-    if (warp == 0) {
-        int at = 0;
-        uint32_t k = lane < kLpWarps ? list_key[lane][0] : 0, j = lane < kLpWarps ? list_idx[lane][0] : 0xFFFFFFFFu;
-        for (int i = 0; i < a.n_top; ++i) {
-            uint32_t bk, bj;
-            warp_best(k, j, &bk, &bj);
-            if (lane == 0) {
-                a.top_idx[r * a.n_top + i] = (int32_t)bj;
-                a.top_logp[r * a.n_top + i] = logp_of(value_of(bk));
+    if (sorted) {
+        // The general way, whose work does not depend on the logits: the n best chunks ...
+        WarpList list;
+        list.init();
+        for (int g = warp * 32; g < chunks; g += warps * 32)
+            take(list, g + lane < chunks ? chunk_max[g + lane] : 0u, g + lane < chunks ? g + lane : kNone);
+        merge_lists(list, min(warps, (chunks + 31) / 32));
+        if (warp == 0) sel[lane] = list.idx;
+        __syncthreads();
+        // ... the n best vectors of those ...
+        list.init();
+        const int picked = min(n, chunks) * kLpUnroll;
+        for (int i = warp; i < picked; i += warps) {
+            const int v = (g_first + (int)sel[i / kLpUnroll]) * kLpChunk + i % kLpUnroll * 32 + lane;
+            uint32_t key = 0u;
+            if (v < row.nvec) {
+                float x[VEC];
+                RowView<T>::unpack(row.load(v, -INFINITY), x);
+                float mx = x[0];
+#pragma unroll
+                for (int e = 1; e < VEC; ++e) mx = fmaxf(mx, x[e]);
+                key = max(order_of(mx), 1u);
             }
-            if (j == bj && lane < kLpWarps) {
-                ++at;
-                k = at < a.n_top ? list_key[lane][at] : 0;
-                j = at < a.n_top ? list_idx[lane][at] : 0xFFFFFFFFu;
+            take(list, key, v < row.nvec ? (uint32_t)v : kNone);
+        }
+        __syncthreads();                                     // sel has been read
+        merge_lists(list, min(warps, picked));
+        if (warp == 0) sel[lane] = list.idx;
+        __syncthreads();
+        // ... and the n best logits of those
+        list.init();
+        for (int i = warp * 32 + lane; i - lane < n * VEC; i += warps * 32) {
+            uint32_t key = 0u, idx = kNone;
+            if (i < n * VEC && sel[i / VEC] != kNone) {
+                const int j = row.first((int)sel[i / VEC]) + i % VEC;
+                if (j >= 0 && j < a.V) key = order_of(to_f32<T>(row.p[j])), idx = (uint32_t)j;
+            }
+            take(list, key, idx);
+        }
+        merge_lists(list, min(warps, (n * VEC + 31) / 32));
+        if (warp == 0 && lane < n) put(lane, list.key, list.idx);
+    }
+    if (ctas > 1) {
+        // the CTAs' lists, n entries each, by comparing all of them
+        cluster_sync();
+        if (rank == 0) {
+            const int all = n * (int)ctas;                   // <= kLpCandidates
+            for (int i = threadIdx.x; i < all; i += blockDim.x)
+                candidates[i] = ld_cluster_u64(&cta_list[i % n], i / n);
+            __syncthreads();
+            for (int i = threadIdx.x; i < all; i += blockDim.x) {
+                const uint64_t own = candidates[i];
+                int place = 0;
+                for (int o = 0; o < all; ++o) place += candidates[o] > own;
+                if (place < n && own != pack_entry(0u, kNone)) write_top(place, (uint32_t)(own >> 32), ~(uint32_t)own);
             }
         }
+        cluster_sync();                                      // remote lists and sums have been read
     }
+}
+
+template <typename T>
+static auto pick_logprobs(int id_bytes, bool wide) -> void (*)(LogprobArgs) {
+    if (wide) return id_bytes == 8 ? logprobs_kernel<T, int64_t, 32> : logprobs_kernel<T, int32_t, 32>;
+    return id_bytes == 8 ? logprobs_kernel<T, int64_t, 8> : logprobs_kernel<T, int32_t, 8>;
 }
 
 cudaError_t launch_token_logprobs(const LogprobCall& c, cudaStream_t stream) {
     if (c.T == 0) return cudaSuccess;
-    LogprobArgs a{c.logits, c.V, c.ld, c.scale, c.targets, c.logp, c.entropy, c.stats, c.n_top, c.top_idx, c.top_logp,
-                  c.ws};
-    const int vec = 16 / (int)dtype_bytes(c.dtype);
-    const size_t smem = c.n_top ? sizeof(uint32_t) * (size_t)((c.V + vec) / (32 * vec) + 1) : 0;
-    void (*k)(LogprobArgs) =
-        c.dtype == MOE_F32 ? (c.id_bytes == 8 ? logprobs_kernel<float, int64_t> : logprobs_kernel<float, int32_t>)
-                           : (c.id_bytes == 8 ? logprobs_kernel<uint16_t, int64_t> : logprobs_kernel<uint16_t, int32_t>);
-    cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (err != cudaSuccess) return err;
-    k<<<(unsigned)c.T, kLpThreads, smem, stream>>>(a);
-    return cudaGetLastError();
+    LogprobArgs a{c.logits, (int)c.V, c.ld, c.scale, !fast_scale(c.scale), c.targets, c.logp,
+                  c.entropy, c.stats, c.n_top, c.top_idx, c.top_logp, c.ws};
+    const int64_t vec = 16 / (int64_t)dtype_bytes(c.dtype);
+    const int64_t chunks = (c.V + 2 * vec - 2) / (vec * kLpChunk) + 1;         // at most, at any alignment
+    // One warp per chunk, up to eight.  While there are SMs to spare a row is spread over a
+    // cluster, and where even that leaves most of them idle its CTAs have up to 32 warps.
+    int warps = 1, ctas = 1;
+    while (warps < 8 && warps < chunks) warps *= 2;
+    while (ctas < kLpMaxCluster && chunks > (int64_t)warps * ctas && c.T * ctas * 2 <= 4 * (int64_t)c.num_sms) ctas *= 2;
+    const bool wide = ctas == kLpMaxCluster && c.T * ctas <= c.num_sms && chunks > 8 * ctas;
+    while (wide && warps < kLpMaxWarps && chunks > (int64_t)warps * ctas) warps *= 2;
+    const size_t smem = c.n_top ? sizeof(uint32_t) * (size_t)((chunks + ctas - 1) / ctas + 4) : 0;
+    void (*k)(LogprobArgs) = c.dtype == MOE_F32 ? pick_logprobs<float>(c.id_bytes, wide)
+                                                : pick_logprobs<uint16_t>(c.id_bytes, wide);
+    cudaLaunchConfig_t cfg{};
+    if (c.T * ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+    cfg.gridDim = dim3((unsigned)(c.T * ctas));
+    cfg.blockDim = dim3(32 * warps);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = ctas;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, a);
 }
 
 // ------------------------------------------------------------------------ gradient
-// One thread per vector of a row, blockIdx.y strides over the rows.  dlogits may be the
-// logits' own buffer: a thread reads its elements before it writes them.
+// d x_j = p_j (g1 + g2 lp_j) + 1[j = t] scale g_logp with g2 = -scale g_entropy and
+// g1 = -scale (g_logp + g_entropy entropy).  dlogits may be the logits' own buffer: a thread
+// reads its elements before it writes them.  The kernel moves each logit in and its
+// gradient out once and is to be HBM-bound, which leaves it about 20 instructions per BF16
+// logit: whole blocks of a row away from its ends and its target take a path without checks
+// (6 per logit).
 struct LogprobGradArgs {
     const void* logits;
-    int64_t T, V, ld;
+    int64_t T;
+    int V;
+    int64_t ld;
     float scale;
+    int careful;              // the scale is outside the fast path's range
     const void* targets;
     const float *stats, *entropy, *g_logp, *g_entropy;
     void* dlogits;
     int64_t ld_d;
+    int blocks_per_row;
     WsHeader* ws;
 };
+constexpr int kGradThreads = 128, kGradUnroll = 4;
+constexpr int kGradVectors = kGradThreads * kGradUnroll;
+
+struct GradRow {
+    float m, scale, ls, g1, g2;
+};
+// 2^y as the square of 2^(y/2): probabilities below FP32's normal numbers keep their bits, at
+// the price of one multiplication (the factor they meet may be large).
+__device__ __forceinline__ F2 grad_pair(F2 x, const GradRow& g) {
+    const F2 lp = f2_fma(f2_add(x, f2(-g.m, -g.m)), f2(g.scale, g.scale), f2(-g.ls, -g.ls));
+    float y0, y1;
+    f2_split(f2_mul(lp, f2(0.5f * kLog2e, 0.5f * kLog2e)), y0, y1);
+    const F2 e = f2(exp2_approx(y0), exp2_approx(y1));
+    return f2_mul(f2_mul(e, e), f2_fma(lp, f2(g.g2, g.g2), f2(g.g1, g.g1)));
+}
+// The same for any logit: a masked one, whose 0 * -inf is 0 here, and any row.
+__device__ __forceinline__ float grad_one(float x, const GradRow& g) {
+    float lp = (x - g.m) * g.scale - g.ls;
+    if (lp < -1e4f) lp = -1e4f;                                      // NaN stays
+    const float e = exp2_approx(lp * (0.5f * kLog2e));
+    return e * e * fmaf(lp, g.g2, g.g1);
+}
 
 template <typename T, typename Id, bool VECTOR>
-__global__ void __launch_bounds__(256) logprobs_grad_kernel(const __grid_constant__ LogprobGradArgs a) {
-    const int64_t groups = (a.V + 7) / 8;
-    for (int64_t b = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; b < a.T * groups;
-         b += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t r = b / groups, j = (b % groups) * 8;
-        const int n = (int)(a.V - j < 8 ? a.V - j : 8);
-        const float m = a.stats[2 * r], ls = a.stats[2 * r + 1];
-        const bool empty = ls == -INFINITY;
-        float gl = 0.f, ge = 0.f, h = 0.f;
-        int64_t t = -1;
-        if (a.g_logp) {
-            t = (int64_t)((const Id*)a.targets)[r];
-            if (t >= a.V) {
-                if (j == 0) set_status(a.ws, MOE_ERR_DEVICE_CHECK);
-                t = -1;
-            }
-            if (t >= 0) gl = a.g_logp[r] * a.scale;
-        }
-        if (a.g_entropy) ge = a.g_entropy[r] * a.scale, h = a.entropy[r];
-        float x[8];
-        load8<T, VECTOR>((const T*)a.logits + r * a.ld + j, n, x);
+__global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const __grid_constant__ LogprobGradArgs a) {
+    constexpr int VEC = RowView<T>::VEC;
+    // the last rows first: they are the ones a forward pass has left in L2 (0.5% faster)
+    const int64_t r = a.T - 1 - blockIdx.x / (unsigned)a.blocks_per_row;
+    const int v0 = (int)(blockIdx.x % (unsigned)a.blocks_per_row) * kGradVectors;
+    const T* in = (const T*)a.logits + r * a.ld;
+    T* out = (T*)a.dlogits + r * a.ld_d;
+    // logits and gradient rows of the same alignment: vectors of that alignment, their loads
+    // before the row's numbers are waited for
+    const RowView<T> row(in, a.V);
+    const bool inside = VECTOR && row.whole(v0) && row.whole(v0 + kGradVectors - 1);
+    const T* p = in + row.first(v0) + (int)threadIdx.x * VEC;
+    uint4 q[kGradUnroll];
+    if (inside) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const bool off = empty || x[i] == -INFINITY;
-            const float lp = (x[i] - m) * a.scale - ls;
-            const float p = exp2_full(lp * kLog2e);
-            const float d = -p * fmaf(ge, fmaxf(lp, -1e4f) + h, gl) + (j + i == t ? gl : 0.f);
-            x[i] = off ? 0.f : d;
+        for (int u = 0; u < kGradUnroll; ++u) q[u] = ld_v4(p + u * (kGradThreads * VEC));
+    }
+    GradRow g;
+    g.m = a.stats[2 * r];
+    g.ls = a.stats[2 * r + 1];
+    g.scale = a.scale;
+    int t = -1;
+    float gl = 0.f, ge = 0.f, h = 0.f;
+    if (a.g_logp) {
+        const Id target = ((const Id*)a.targets)[r];
+        gl = a.g_logp[r] * a.scale;
+        if (target >= 0 && (int64_t)target < a.V) t = (int)target;
+        else gl = 0.f;
+        if ((int64_t)target >= a.V && v0 == 0 && threadIdx.x == 0) set_status(a.ws, MOE_ERR_DEVICE_CHECK);
+    }
+    if (a.g_entropy) ge = a.g_entropy[r] * a.scale, h = a.entropy[r];
+    const bool empty = g.ls == -INFINITY;                            // masked throughout: no gradient
+    g.g2 = -ge;
+    g.g1 = -fmaf(ge, h, gl);
+    const bool special = empty || a.careful || !(fabsf(g.m) < kFastMax) || fabsf(ge) > 1e6f ||
+                         (t >= row.first(v0) && t < row.first(v0 + kGradVectors));
+    if (inside && !special) {
+        T* o = out + row.first(v0) + (int)threadIdx.x * VEC;
+#pragma unroll
+        for (int u = 0; u < kGradUnroll; ++u) {
+            const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+            uint32_t d[4];
+            if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t f = floor_bf16x2(w[i]);
+                    float d0, d1;
+                    f2_split(grad_pair(f2(__uint_as_float(f << 16), __uint_as_float(f & 0xFFFF0000u)), g), d0, d1);
+                    d[i] = pack_bf16x2(d0, d1);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    float d0, d1;
+                    f2_split(grad_pair(f2(floor_f32(__uint_as_float(w[i])), floor_f32(__uint_as_float(w[i + 1]))), g),
+                             d0, d1);
+                    d[i] = __float_as_uint(d0), d[i + 1] = __float_as_uint(d1);
+                }
+            }
+            st_v4(o + u * (kGradThreads * VEC), make_uint4(d[0], d[1], d[2], d[3]));
         }
-        store8<T, VECTOR>((T*)a.dlogits + r * a.ld_d + j, n, x);
+        return;
+    }
+    // element by element, neighbouring lanes on neighbouring elements, eight loads at a time
+    const int first = VECTOR ? row.first(v0) : v0 * VEC;
+    const int j1 = min(a.V, first + kGradVectors * VEC);
+    constexpr int E = 8;
+    for (int j0 = max(first, 0) + (int)threadIdx.x; j0 < j1; j0 += E * kGradThreads) {
+        T x[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            if (j0 + i * kGradThreads < j1) x[i] = in[j0 + i * kGradThreads];
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const int j = j0 + i * kGradThreads;
+            if (j >= j1) continue;
+            float d = grad_one(to_f32<T>(x[i]), g);
+            if (j == t && to_f32<T>(x[i]) != -INFINITY) d += gl;     // a masked target has no part
+            out[j] = from_f32<T>(empty ? 0.f : d);
+        }
     }
 }
 
 template <typename T, typename Id>
-static cudaError_t launch_grad_t(const LogprobGradArgs& a, bool vec, int num_sms, cudaStream_t stream) {
-    const int64_t total = a.T * ((a.V + 7) / 8);
-    int64_t grid = (total + 255) / 256;
-    if (grid > (int64_t)num_sms * 8) grid = (int64_t)num_sms * 8;
+static cudaError_t launch_grad_t(LogprobGradArgs& a, cudaStream_t stream) {
+    constexpr int64_t VEC = 16 / sizeof(T);
+    const bool vec = (((uintptr_t)a.logits - (uintptr_t)a.dlogits) & 15) == 0 &&
+                     ((a.ld - a.ld_d) * (int64_t)sizeof(T)) % 16 == 0;
+    a.blocks_per_row = (int)(((a.V + 2 * VEC - 2) / VEC + kGradVectors - 1) / kGradVectors);
+    const int64_t grid = a.T * a.blocks_per_row;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     auto* k = vec ? logprobs_grad_kernel<T, Id, true> : logprobs_grad_kernel<T, Id, false>;
-    k<<<(unsigned)grid, 256, 0, stream>>>(a);
+    k<<<(unsigned)grid, kGradThreads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
 cudaError_t launch_token_logprobs_backward(const LogprobGradCall& c, cudaStream_t stream) {
     if (c.T == 0) return cudaSuccess;
-    LogprobGradArgs a{c.logits, c.T, c.V, c.ld, c.scale, c.targets, c.stats, c.entropy, c.g_logp, c.g_entropy,
-                      c.dlogits, c.ld_d, c.ws};
-    const bool vec = rows_in_groups(c.logits, c.V, c.ld, c.dtype) && rows_in_groups(c.dlogits, c.V, c.ld_d, c.dtype);
+    LogprobGradArgs a{c.logits, c.T, (int)c.V, c.ld, c.scale, !fast_scale(c.scale), c.targets, c.stats, c.entropy, c.g_logp, c.g_entropy,
+                      c.dlogits, c.ld_d, 0, c.ws};
     if (c.dtype == MOE_F32)
-        return c.id_bytes == 8 ? launch_grad_t<float, int64_t>(a, vec, c.num_sms, stream)
-                               : launch_grad_t<float, int32_t>(a, vec, c.num_sms, stream);
-    return c.id_bytes == 8 ? launch_grad_t<uint16_t, int64_t>(a, vec, c.num_sms, stream)
-                           : launch_grad_t<uint16_t, int32_t>(a, vec, c.num_sms, stream);
+        return c.id_bytes == 8 ? launch_grad_t<float, int64_t>(a, stream) : launch_grad_t<float, int32_t>(a, stream);
+    return c.id_bytes == 8 ? launch_grad_t<uint16_t, int64_t>(a, stream) : launch_grad_t<uint16_t, int32_t>(a, stream);
 }
 
 }  // namespace moe
