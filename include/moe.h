@@ -528,8 +528,8 @@ int moe_embedding(const void* ids, int id_bytes, int64_t N, const void* table, i
 
 /* Gradient of the embedding table, by tokens sorted by id:
  *   dtable[v] = scale * sum over n with ids[n] = v of dout[n]   (+ dtable[v], accumulate)
- * summed in token order in FP32 (ranges of 4 to 32 sorted tokens, by N and H alone, then
- * the ranges in order).
+ * summed in FP32, in token order within ranges of 4 to 32 sorted tokens (by N and H
+ * alone) and in an order set by their number over the ranges.
  * Without `accumulate` every row of dtable is written, zeros where no token names it;
  * with it only the rows that tokens name are touched.  Negative ids take no part; an id
  * of V or more takes none and records MOE_ERR_DEVICE_CHECK.

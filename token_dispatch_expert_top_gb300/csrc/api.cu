@@ -283,7 +283,7 @@ int check_status_ws(void* ws, size_t bytes) {
 
 // Workspace regions of moe_embedding_backward, in order.
 struct EmbedPlan {
-    size_t n_live, order, key, present, part, total;
+    size_t n_live, crossing, order, key, present, part, total;
 };
 
 EmbedPlan make_embed_plan(int64_t N, int64_t V, int64_t H) {
@@ -294,7 +294,8 @@ EmbedPlan make_embed_plan(int64_t N, int64_t V, int64_t H) {
         off += align256(bytes);
         return o;
     };
-    pl.n_live = take(sizeof(int32_t));
+    pl.n_live = take(2 * sizeof(int32_t));
+    pl.crossing = take(sizeof(int32_t) * (size_t)embed_ranges(N, H));
     pl.order = take(sizeof(int32_t) * (size_t)N);
     pl.key = take(sizeof(int32_t) * (size_t)N);
     pl.present = take(sizeof(uint32_t) * (size_t)((V + 31) / 32));
@@ -1106,6 +1107,7 @@ int moe_embedding_backward(const void* ids, int id_bytes, int64_t N, int64_t V, 
     c.order = at<int32_t>(workspace, pl.order);
     c.key = at<int32_t>(workspace, pl.key);
     c.n_live = at<int32_t>(workspace, pl.n_live);
+    c.crossing = at<int32_t>(workspace, pl.crossing);
     c.present = at<uint32_t>(workspace, pl.present);
     c.part = at<float>(workspace, pl.part);
     c.num_sms = num_sms_current();

@@ -11,41 +11,37 @@
 
 namespace moe {
 
-// Ten rounds on the counter (x0, x1, x2, x3) under the key (k0, k1).
-__device__ __forceinline__ void philox_10(uint32_t (&x)[4], uint32_t k0, uint32_t k1) {
-#pragma unroll
-    for (int i = 0; i < 10; ++i) {
-        const uint64_t a = (uint64_t)x[0] * 0xD2511F53u, b = (uint64_t)x[2] * 0xCD9E8D57u;
-        x[0] = (uint32_t)(b >> 32) ^ x[1] ^ k0;
-        x[1] = (uint32_t)b;
-        x[2] = (uint32_t)(a >> 32) ^ x[3] ^ k1;
-        x[3] = (uint32_t)a;
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
-    }
-}
-
-// Bit i: element i of the counter's eight is kept.
-__device__ __forceinline__ uint32_t keep_bits(uint64_t b, uint32_t thr, uint64_t seed, uint64_t offset) {
-    uint32_t w[4] = {(uint32_t)b, (uint32_t)(b >> 32), (uint32_t)offset, (uint32_t)(offset >> 32)};
-    philox_10(w, (uint32_t)seed, (uint32_t)(seed >> 32));
-    uint32_t keep = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        keep |= (uint32_t)((w[i] & 0xFFFFu) >= thr) << (2 * i) | (uint32_t)((w[i] >> 16) >= thr) << (2 * i + 1);
-    return keep;
-}
-
 struct DropoutArgs {
     const void *x, *residual;
     void* out;
     int64_t ld_x, ld_res, ld_out;
     int64_t rows, cols;
     int64_t groups;             // per row: ceil(cols / 8)
-    uint32_t thr;
+    uint32_t thr_high;          // thr << 16
+    int drop_all;               // thr = 65536
     float keep_scale;
-    uint64_t seed, offset;
+    uint64_t offset;
+    uint32_t key[10][2];        // the rounds' keys: seed + round * Weyl constants
 };
+
+// The generator's ten rounds on the counter (b, offset): one wide multiplication and one
+// three-way exclusive or per word, the keys from the kernel's arguments.
+__device__ __forceinline__ void philox_10(uint64_t b, const DropoutArgs& a, uint32_t (&x)[4]) {
+    x[0] = (uint32_t)b, x[1] = (uint32_t)(b >> 32), x[2] = (uint32_t)a.offset, x[3] = (uint32_t)(a.offset >> 32);
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+        const uint64_t p = (uint64_t)x[0] * 0xD2511F53u, q = (uint64_t)x[2] * 0xCD9E8D57u;
+        x[0] = (uint32_t)(q >> 32) ^ x[1] ^ a.key[i][0];
+        x[1] = (uint32_t)q;
+        x[2] = (uint32_t)(p >> 32) ^ x[3] ^ a.key[i][1];
+        x[3] = (uint32_t)p;
+    }
+}
+// Whether element i of the counter's eight is kept: its 16 bits, moved to the top of a word
+// (what lies below them does not matter), against thr there.
+__device__ __forceinline__ bool kept(const uint32_t (&w)[4], int i, const DropoutArgs& a) {
+    return (i % 2 ? w[i / 2] : w[i / 2] << 16) >= a.thr_high;
+}
 
 // The residual and x may each be `out` itself: every thread reads its own elements before it
 // writes them.
@@ -55,8 +51,13 @@ struct DropoutArgs {
 template <typename T>
 __global__ void __launch_bounds__(256) dropout_groups_kernel(const __grid_constant__ DropoutArgs a) {
     const uint64_t b = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-    const uint64_t r = b >> 32 || a.groups >> 32 ? b / (uint64_t)a.groups : (uint32_t)b / (uint32_t)a.groups;
-    if (r >= (uint64_t)a.rows) return;
+    uint64_t r = 0;
+    if (a.rows == 1) {
+        if (b >= (uint64_t)a.groups) return;
+    } else {
+        r = b >> 32 || a.groups >> 32 ? b / (uint64_t)a.groups : (uint32_t)b / (uint32_t)a.groups;
+        if (r >= (uint64_t)a.rows) return;
+    }
     const int64_t c = (int64_t)(b - r * a.groups) * 8;
     float v[8], y[8];
     load8<T, true>((const T*)a.x + r * a.ld_x + c, 8, v);
@@ -66,10 +67,13 @@ __global__ void __launch_bounds__(256) dropout_groups_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = 0.f;
     }
-    const uint32_t keep = keep_bits(b, a.thr, a.seed, a.offset);
+    uint32_t w[4];
+    philox_10(b, a, w);
+    if (!a.drop_all) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (keep >> i & 1) y[i] = fmaf(v[i], a.keep_scale, y[i]);
+        for (int i = 0; i < 8; ++i)
+            if (kept(w, i, a)) y[i] = fmaf(v[i], a.keep_scale, y[i]);
+    }
     store8<T, true>((T*)a.out + r * a.ld_out + c, 8, y);
 }
 
@@ -93,7 +97,12 @@ __global__ void __launch_bounds__(256) dropout_columns_kernel(const __grid_const
         v[i] = in ? to_f32<T>(x[i * 32]) : 0.f;
         y[i] = in && a.residual ? to_f32<T>(res[i * 32]) : 0.f;
     }
-    const uint32_t mine = keep_bits((uint64_t)(r * a.groups + c0 / 8 + lane), a.thr, a.seed, a.offset);
+    uint32_t w[4], mine = 0;                    // bit i: element i of this lane's counter is kept
+    philox_10((uint64_t)(r * a.groups + c0 / 8 + lane), a, w);
+    if (!a.drop_all) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mine |= (uint32_t)kept(w, i, a) << i;
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const uint32_t keep = __shfl_sync(0xffffffffu, mine, 4 * i + lane / 8);
@@ -106,10 +115,24 @@ cudaError_t launch_dropout(const void* x, int dtype, int64_t rows, int64_t cols,
                            int64_t ld_res, uint32_t thr, uint64_t seed, uint64_t offset, void* out, int64_t ld_out,
                            cudaStream_t stream) {
     if (rows == 0 || cols == 0) return cudaSuccess;
-    DropoutArgs a{x, residual, out, ld_x, ld_res, ld_out, rows, cols, (cols + 7) / 8, thr,
-                  thr < 65536u ? (float)(65536.0 / (65536.0 - thr)) : 0.f, seed, offset};
     const bool vec = rows_in_groups(x, cols, ld_x, dtype) && rows_in_groups(out, cols, ld_out, dtype) &&
                      (!residual || rows_in_groups(residual, cols, ld_res, dtype));
+    if (vec && ld_x == cols && ld_out == cols && (!residual || ld_res == cols) && rows <= (1ll << 60) / cols) {
+        cols *= rows;                           // one long row has the same counters
+        rows = 1;
+    }
+    DropoutArgs a{};
+    a.x = x, a.residual = residual, a.out = out;
+    a.ld_x = ld_x, a.ld_res = ld_res, a.ld_out = ld_out;
+    a.rows = rows, a.cols = cols, a.groups = (cols + 7) / 8;
+    a.thr_high = thr << 16;
+    a.drop_all = thr >= 65536u;
+    a.keep_scale = a.drop_all ? 0.f : (float)(65536.0 / (65536.0 - thr));
+    a.offset = offset;
+    for (uint32_t i = 0; i < 10; ++i) {
+        a.key[i][0] = (uint32_t)seed + i * 0x9E3779B9u;
+        a.key[i][1] = (uint32_t)(seed >> 32) + i * 0xBB67AE85u;
+    }
     if (rows > (1ll << 60) / a.groups) return cudaErrorInvalidValue;
     if (vec) {
         const int64_t grid = (rows * a.groups + 255) / 256;

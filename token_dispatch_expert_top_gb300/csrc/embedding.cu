@@ -14,7 +14,8 @@
 //      summed in FP32 in token order and written, a run that crosses a range's end leaves
 //      an FP32 partial row.  (Before it embed_fill_kernel sets the rows no token names to
 //      zero, unless the caller accumulates.)
-//   3. embed_join_kernel: adds the partial rows of each run that crossed, in order.
+//   3. embed_join_kernel: adds the partial rows of each run that crossed, in an order that
+//      its length alone sets.
 #include "kernels.cuh"
 #include "vec_io.cuh"
 
@@ -197,29 +198,80 @@ __device__ __forceinline__ int block_scan_exclusive(int v, int* warp_sums, int* 
     return before + incl - v;
 }
 
-// The sorted list's places for the CTA's own tokens list_row / list_pos [0, n), which are in
-// token order: by one warp, 32 at a time; cursor[row] is the row's next place.
-__device__ __forceinline__ void place_list(const int* list_row, const int* list_pos, int n, int* cursor, int v0,
-                                           int32_t* order, int32_t* key) {
-    const int lane = threadIdx.x % 32;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-        const int i = i0 + lane;
-        const int row = i < n ? list_row[i] : -1 - lane;
-        const unsigned same = __match_any_sync(0xffffffffu, row);
-        if (row >= 0) {
-            const int place = cursor[row] + __popc(same & ((1u << lane) - 1u));
-            order[place] = list_pos[i];
-            key[place] = v0 + row;
+// Gives the CTA's own tokens list_row / list_pos [0, n), which are in token order, their places
+// in the sorted list; cursor[row] is the row's next place.  All threads call it.
+//   Short lists: one warp, 32 tokens at a time.  Long ones (a frequent token): kPlaceWarps
+// warps count their shares' tokens by row, the counts are summed up over the warps, and
+// every token's place is its row's, its warp's and its own rank.
+constexpr int kPlaceWarps = 8, kPlaceShare = kOrderList / kPlaceWarps, kPlaceSerial = 512;
+__device__ __forceinline__ void place_list(int* list_row, const int* list_pos, int n, int* cursor, uint16_t* counts,
+                                           int rows, int v0, int32_t* order, int32_t* key) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    if (n <= kPlaceSerial) {
+        if (warp == 0) {
+            for (int i0 = 0; i0 < n; i0 += 32) {
+                const int i = i0 + lane;
+                const int row = i < n ? list_row[i] : -1 - lane;
+                const unsigned same = __match_any_sync(0xffffffffu, row);
+                if (row >= 0) {
+                    const int place = cursor[row] + __popc(same & ((1u << lane) - 1u));
+                    order[place] = list_pos[i];
+                    key[place] = v0 + row;
+                }
+                __syncwarp();
+                if (row >= 0 && lane == 31 - __clz(same)) cursor[row] += __popc(same);
+                __syncwarp();
+            }
         }
-        __syncwarp();
-        if (row >= 0 && lane == 31 - __clz(same)) cursor[row] += __popc(same);
-        __syncwarp();
+        __syncthreads();
+        return;
     }
+    for (int i = threadIdx.x; i < kPlaceWarps * rows; i += blockDim.x) counts[i] = 0;
+    __syncthreads();
+    if (warp < kPlaceWarps) {
+        uint16_t* mine = counts + warp * rows;
+        const int end = min(n, (warp + 1) * kPlaceShare);
+        for (int i0 = warp * kPlaceShare; i0 < end; i0 += 32) {
+            const int i = i0 + lane;
+            const int row = i < end ? list_row[i] : -1 - lane;
+            const unsigned same = __match_any_sync(0xffffffffu, row);
+            if (row >= 0) list_row[i] = row | (mine[row] + __popc(same & ((1u << lane) - 1u))) << 16;
+            __syncwarp();
+            if (row >= 0 && lane == 31 - __clz(same)) mine[row] += __popc(same);
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    for (int row = threadIdx.x; row < rows; row += blockDim.x) {
+        int sum = 0;
+        for (int w = 0; w < kPlaceWarps; ++w) {
+            const int c = counts[w * rows + row];
+            counts[w * rows + row] = (uint16_t)sum;
+            sum += c;
+        }
+        counts[kPlaceWarps * rows + row] = (uint16_t)sum;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const int row = list_row[i] & 0xFFFF, rank = list_row[i] >> 16;
+        const int place = cursor[row] + counts[i / kPlaceShare * rows + row] + rank;
+        order[place] = list_pos[i];
+        key[place] = v0 + row;
+    }
+    __syncthreads();
+    for (int row = threadIdx.x; row < rows; row += blockDim.x) cursor[row] += counts[kPlaceWarps * rows + row];
+    __syncthreads();
+}
+constexpr int kOrderRange = 2048;             // ids of a CTA at most
+static_assert(kOrderRange <= 1 << 16 && kOrderList <= 1 << 15, "rows and ranks are packed into a word");
+// Dynamic shared memory of embed_order_kernel: the list, `range` next places and the counts.
+inline size_t order_smem(int range) {
+    return sizeof(int) * (2 * (size_t)kOrderList + range) + sizeof(uint16_t) * (size_t)(kPlaceWarps + 1) * range;
 }
 
 // CTA b places the tokens whose ids lie in [b * range, (b + 1) * range): order[i] is the
 // token at place i of the list sorted by (id, token), key[i] its id; bit v of `present` says
-// that a token names v.  range is a multiple of 32.  Shared memory: `range` counters.
+// that a token names v.  range is a multiple of 32.
 //   One sweep over the ids counts the CTA's own tokens by id, counts the live tokens below
 // its range (where its part of the list begins) and lists its own tokens in order; if the
 // list overflows, a second sweep places them piece by piece.
@@ -229,9 +281,10 @@ __global__ void __launch_bounds__(kOrderThreads)
                        int32_t* __restrict__ key, int32_t* __restrict__ n_live, uint32_t* __restrict__ present,
                        WsHeader* ws) {
     grid_dependents_launch();
-    extern __shared__ int cursor[];
+    extern __shared__ int smem[];
     __shared__ int warp_sums[kOrderThreads / 32];
-    __shared__ int list_row[kOrderList], list_pos[kOrderList];
+    int *list_row = smem, *list_pos = list_row + kOrderList, *cursor = list_pos + kOrderList;
+    uint16_t* counts = reinterpret_cast<uint16_t*>(cursor + range);
     constexpr int kSweep = kOrderThreads * kOrderIds;
     static_assert(kSweep <= kOrderList, "a sweep's own tokens fit the list");
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -281,7 +334,7 @@ __global__ void __launch_bounds__(kOrderThreads)
     int base, all_live;
     block_scan_exclusive(below, warp_sums, &base);
     block_scan_exclusive(live, warp_sums, &all_live);
-    if (blockIdx.x == 0 && tid == 0) *n_live = all_live;
+    if (blockIdx.x == 0 && tid == 0) n_live[0] = all_live, n_live[1] = 0;
     // counts -> first places, and the rows' presence
     __syncthreads();
     int run = base;
@@ -297,7 +350,7 @@ __global__ void __launch_bounds__(kOrderThreads)
     }
     __syncthreads();
     if (listed <= kOrderList) {
-        if (warp == 0) place_list(list_row, list_pos, listed, cursor, v0, order, key);
+        place_list(list_row, list_pos, listed, cursor, counts, rows, v0, order, key);
         return;
     }
     for (int n0 = 0; n0 < N; n0 += kSweep) {
@@ -314,8 +367,7 @@ __global__ void __launch_bounds__(kOrderThreads)
                 list_pos[at++] = n0 + tid * kOrderIds + i;
             }
         __syncthreads();
-        if (warp == 0) place_list(list_row, list_pos, total, cursor, v0, order, key);
-        // the next round's scan begins with a barrier before the list is written again
+        place_list(list_row, list_pos, total, cursor, counts, rows, v0, order, key);
     }
 }
 
@@ -341,7 +393,8 @@ __device__ __forceinline__ float* partial_row(float* part, int64_t range, int wh
 struct EmbedSumArgs {
     const int32_t* order;
     const int32_t* key;
-    const int32_t* n_live;
+    int32_t* n_live;          // [0] tokens with an id, [1] runs that cross a range's end
+    int32_t* crossing;        // the ranges that those runs begin in, in any order
     const void* dout;
     int64_t ld_dout, H;
     float scale;
@@ -459,9 +512,10 @@ __global__ void __launch_bounds__(kSumWarps * 32) embed_segment_kernel(const __g
                 if (k != k_next || i + 1 == cnt) {
                     if (from_before)
                         store_cols<float, VECTOR>(partial_row(a.part, range, 0, Hp), c0, lane, a.H, sum);
-                    else if (k == k_next)
+                    else if (k == k_next) {
                         store_cols<float, VECTOR>(partial_row(a.part, range, 1, Hp), c0, lane, a.H, sum);
-                    else
+                        if (c0 == 0 && lane == 0) a.crossing[atomicAdd(a.n_live + 1, 1)] = range;
+                    } else
                         write_row<Grad, VECTOR>((Grad*)a.dtable, a.ld, k, c0, lane, a.H, sum, a.scale, a.accumulate);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) sum[j] = 0.f;
@@ -472,59 +526,81 @@ __global__ void __launch_bounds__(kSumWarps * 32) embed_segment_kernel(const __g
     }
 }
 
-// One warp per (range, 256 columns): if the range's last run begins in it and goes on, the
-// run's partial rows are added in order and written.
+// The runs that cross ranges, kJoinCols * 256 columns of one at a time per CTA: the run's
+// partial rows are cut into kJoinParts parts, one warp each, and the parts' sums are added in
+// order.  (The runs are listed in any order; each one's sum does not depend on it.)
+constexpr int kJoinCols = 4, kJoinParts = 4;
 template <typename Grad, bool VECTOR>
-__global__ void __launch_bounds__(kSumWarps * 32) embed_join_kernel(const __grid_constant__ EmbedSumArgs a) {
+__global__ void __launch_bounds__(kJoinCols * kJoinParts * 32, 2)
+    embed_join_kernel(const __grid_constant__ EmbedSumArgs a) {
+    __shared__ float sums[kJoinParts - 1][kJoinCols][8][32];
     grid_dependency_wait();
-    const int lane = threadIdx.x % 32;
-    const int64_t item = (int64_t)blockIdx.x * kSumWarps + threadIdx.x / 32;
-    if (item >= (int64_t)a.ranges * a.chunks) return;
-    const int range = (int)(item / a.chunks);
-    const int live = *a.n_live;
-    const int p0 = range * a.places, p1 = p0 + a.places;
-    if (p1 >= live) return;                                       // nothing follows this range
-    const int k = a.key[p1 - 1];
-    if (a.key[p1] != k) return;                                   // the last run ends here
-    if (a.key[p0] == k && p0 > 0 && a.key[p0 - 1] == k) return;   // it began in an earlier range
-    const int64_t c0 = (item - (int64_t)range * a.chunks) * 256;
+    const int lane = threadIdx.x % 32, col = threadIdx.x / 32 % kJoinCols, part = threadIdx.x / 32 / kJoinCols;
+    const int live = a.n_live[0];
+    const int groups = (a.chunks + kJoinCols - 1) / kJoinCols;
+    const int64_t items = (int64_t)a.n_live[1] * groups;
     const int64_t Hp = (a.H + 7) / 8 * 8;
-    float sum[8];
-    load_cols<float, VECTOR>(partial_row(a.part, range, 1, Hp), c0, lane, a.H, sum);
-    for (int r0 = range + 1;; r0 += 32) {
-        // equal ids are neighbours: the run covers the next ranges as long as they begin with it
-        const int64_t first = (int64_t)(r0 + lane) * a.places;
-        const unsigned in = __ballot_sync(0xffffffffu, first < live && a.key[first] == k);
-        const int n = in == 0xffffffffu ? 32 : __ffs(~in) - 1;
-        constexpr int U = 8;
-        for (int i0 = 0; i0 < n; i0 += U) {
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int range = a.crossing[item / groups];
+        const int64_t c0 = ((item % groups) * kJoinCols + col) * 256;
+        const int k = a.key[(range + 1) * a.places - 1];
+        // equal ids are neighbours: the run covers the next ranges as long as they begin with
+        // it; the first that does not, by 32 looks at a time
+        int lo = range + 2, hi = a.ranges;                        // range + 1 begins with it
+        while (lo < hi) {
+            const int step = (hi - lo + 31) / 32;
+            const int64_t r = lo + (int64_t)lane * step;
+            const bool in = r < hi && r * a.places < live && a.key[r * a.places] == k;
+            const int n = __popc(__ballot_sync(0xffffffffu, in));
+            if (n == 0) break;
+            hi = min(hi, lo + n * step);
+            lo = lo + (n - 1) * step + 1;
+        }
+        const int rows = lo - range;                              // partial rows: [range][1], then [r][0]
+        const int first = (int)((int64_t)rows * part / kJoinParts), last = (int)((int64_t)rows * (part + 1) / kJoinParts);
+        float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        constexpr int U = 4;
+        for (int i0 = first; i0 < last && c0 < a.H; i0 += U) {
             float v[U][8];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (i0 + u < n)
-                    load_cols<float, VECTOR>(partial_row(a.part, r0 + i0 + u, 0, Hp), c0, lane, a.H, v[u]);
+                if (i0 + u < last)
+                    load_cols<float, VECTOR>(partial_row(a.part, range + i0 + u, i0 + u == 0, Hp), c0, lane, a.H, v[u]);
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (i0 + u < n) {
+                if (i0 + u < last) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) sum[j] += v[u][j];
                 }
         }
-        if (n < 32) break;
+        if (part > 0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sums[part - 1][col][j][lane] = sum[j];
+        }
+        __syncthreads();
+        if (part == 0 && c0 < a.H) {
+#pragma unroll
+            for (int p = 0; p < kJoinParts - 1; ++p)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[j] += sums[p][col][j][lane];
+            write_row<Grad, VECTOR>((Grad*)a.dtable, a.ld, k, c0, lane, a.H, sum, a.scale, a.accumulate);
+        }
+        __syncthreads();
     }
-    write_row<Grad, VECTOR>((Grad*)a.dtable, a.ld, k, c0, lane, a.H, sum, a.scale, a.accumulate);
 }
 
 // ------------------------------------------------------------------------ host side
 template <typename Id>
 static cudaError_t launch_order_t(const EmbedBackward& c, cudaStream_t stream) {
-    // one CTA per SM, ranges of whole words of `present` and at most 2048 ids (8 KB of counters
-    // beside the 32 KB list)
+    // one CTA per SM, ranges of whole words of `present`
     int64_t range = (c.V + c.num_sms - 1) / c.num_sms;
     range = (range + 31) / 32 * 32;
-    if (range > 2048) range = 2048;
+    if (range > kOrderRange) range = kOrderRange;
     const int64_t grid = (c.V + range - 1) / range;
-    embed_order_kernel<Id><<<(unsigned)grid, kOrderThreads, (size_t)range * sizeof(int), stream>>>(
+    cudaError_t err = cudaFuncSetAttribute(embed_order_kernel<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)order_smem(kOrderRange));
+    if (err != cudaSuccess) return err;
+    embed_order_kernel<Id><<<(unsigned)grid, kOrderThreads, order_smem((int)range), stream>>>(
         (const Id*)c.ids, (int)c.N, c.V, (int)range, c.order, c.key, c.n_live, c.present, c.ws);
     return cudaGetLastError();
 }
@@ -537,6 +613,7 @@ static cudaError_t launch_sums_t(const EmbedBackward& c, cudaStream_t stream) {
     a.order = c.order;
     a.key = c.key;
     a.n_live = c.n_live;
+    a.crossing = c.crossing;
     a.dout = c.dout;
     a.ld_dout = c.ld_dout;
     a.H = c.H;
@@ -555,7 +632,8 @@ static cudaError_t launch_sums_t(const EmbedBackward& c, cudaStream_t stream) {
     cudaError_t err = launch_after(k, blocks, kSumWarps * 32, stream, a);
     if (err != cudaSuccess || a.ranges <= 1) return err;          // one range: no run crosses
     auto* j = vec ? embed_join_kernel<Grad, true> : embed_join_kernel<Grad, false>;
-    return launch_after(j, blocks, kSumWarps * 32, stream, a);
+    const int64_t most = (int64_t)(a.ranges - 1) * ((a.chunks + kJoinCols - 1) / kJoinCols);
+    return launch_after(j, most < 2 * c.num_sms ? most : 2 * c.num_sms, kJoinCols * kJoinParts * 32, stream, a);
 }
 
 cudaError_t launch_embedding_backward(const EmbedBackward& c, cudaStream_t stream) {

@@ -191,13 +191,13 @@ struct WarpList {
     }
 };
 
-constexpr int kLpMaxWarps = 32;
+constexpr int kLpMaxWarps = 8;
 constexpr int kLpUnroll = 4;                    // vectors a lane holds at once
 constexpr int kLpChunk = 32 * kLpUnroll;        // vectors a warp reads at once: one chunk
 constexpr int kLpMaxCluster = 8;
-constexpr int kLpRanked = 256;                  // chunks that are ranked by all comparisons
-constexpr int kLpCandidates = 256;              // logits that are
-static_assert(kLpMaxCluster * kMaxTop <= kLpCandidates, "the CTAs' lists are ranked together");
+constexpr int kLpAside = 512;                   // vectors set aside during the pass
+constexpr int kLpRanked = 256;                  // logits whose places are found by comparing all of them
+static_assert(kLpMaxCluster * kMaxTop <= kLpRanked, "the CTAs' lists are ranked together");
 
 struct LogprobArgs {
     const void* logits;
@@ -242,23 +242,24 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(const void* p, uint32_t rank)
     return v;
 }
 
-// Largest logit of the lane's vectors (NaN ignored).
+// Largest logit of a vector (NaN ignored).
 template <typename T>
-__device__ __forceinline__ float lane_max(const uint4 (&q)[kLpUnroll]) {
+__device__ __forceinline__ float vector_max(const uint4& q) {
     if constexpr (sizeof(T) == 2) {
-        uint32_t h = 0xFF80FF80u;               // -inf, -inf
-#pragma unroll
-        for (int u = 0; u < kLpUnroll; ++u)
-            h = max_bf16x2(h, max_bf16x2(max_bf16x2(q[u].x, q[u].y), max_bf16x2(q[u].z, q[u].w)));
+        const uint32_t none = 0xFF80FF80u;      // -inf, -inf
+        const uint32_t h = max_bf16x2(max_bf16x2(max_bf16x2(q.x, q.y), max_bf16x2(q.z, q.w)), none);
         return fmaxf(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u));
     } else {
-        float h = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < kLpUnroll; ++u)
-            h = fmaxf(h, fmaxf(fmaxf(__uint_as_float(q[u].x), __uint_as_float(q[u].y)),
-                               fmaxf(__uint_as_float(q[u].z), __uint_as_float(q[u].w))));
-        return h;
+        return fmaxf(fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)),
+                           fmaxf(__uint_as_float(q.z), __uint_as_float(q.w))), -INFINITY);
     }
+}
+template <typename T>
+__device__ __forceinline__ float lane_max(const uint4 (&q)[kLpUnroll]) {
+    float m = vector_max<T>(q[0]);
+#pragma unroll
+    for (int u = 1; u < kLpUnroll; ++u) m = fmaxf(m, vector_max<T>(q[u]));
+    return m;
 }
 
 // Adds 2^y and y 2^y of the lane's vectors.
@@ -297,21 +298,25 @@ __device__ __forceinline__ void add_vectors(const uint4 (&q)[kLpUnroll], float c
 // One cluster of CTAs per row (each takes a contiguous share of the row's chunks), one pass
 // over the row.  Bound by HBM: 8 loads of 16 bytes per lane are in flight at most, 32 warps
 // an SM; per BF16 logit about 5 instructions are issued, of which one is the exponential.
-// For the top list the pass only keeps the maximum of each chunk (kLpChunk vectors: what a
-// warp reads at once).  The n best logits lie in the n best chunks by (maximum, position): a
-// chunk below those has n chunks before it, each with a logit that beats all of its own.  So
-// n chunks are read again, from L2, and of them only the logits that reach the n-th best
-// maximum matter.  Those are few; where ties and masks make them many, the same argument
-// picks the n best vectors of the n chunks, which are 8 n (FP32: 4 n) logits to sort.
-template <typename T, typename Id, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) logprobs_kernel(const __grid_constant__ LogprobArgs a) {
-    extern __shared__ __align__(16) uint32_t chunk_max[];    // order_of the chunk's maximum, at least 1; four zeros
-    __shared__ RowSums warp_sums[WARPS], cta_sums;
-    __shared__ CarefulSums warp_careful[WARPS], cta_careful;
-    __shared__ uint32_t sel[32], least;
-    __shared__ uint32_t list_key[WARPS][32], list_idx[WARPS][32];
-    __shared__ uint64_t candidates[kLpCandidates], cta_list[32];
-    __shared__ int found;
+// For the top list the pass sets aside, from registers, the vectors with a logit that reaches a
+// bound which rises as it goes; about a hundred for n = 8, of which some 3 n logits reach the
+// last bound and are ranked.  (Reading the best chunks again afterwards cost a trip to DRAM per row, as the rows
+// in flight do not fit L2: 369 against 345 us for 8192 x 127901 BF16 and n = 8.)  Where
+// the logits' order or ties make too many, a way whose work does not depend on the logits is
+// taken: the n best logits lie in the n best chunks (what a warp reads at once) by (maximum,
+// position), as a chunk below those has n chunks before it, each with a logit that beats all
+// of its own; likewise in the n best vectors of these, which are 8 n (FP32: 4 n) logits.
+template <typename T, typename Id, bool TOP>
+__global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __grid_constant__ LogprobArgs a) {
+    extern __shared__ uint32_t chunk_max[];                  // the general way's: order_of the maximum, at least 1
+    __shared__ RowSums warp_sums[kLpMaxWarps], cta_sums;
+    __shared__ CarefulSums warp_careful[kLpMaxWarps], cta_careful;
+    __shared__ uint32_t vote[kLpMaxWarps], sel[32];
+    __shared__ uint32_t list_key[kLpMaxWarps][32], list_idx[kLpMaxWarps][32];
+    __shared__ uint4 aside[kLpAside];
+    __shared__ int aside_v[kLpAside];
+    __shared__ uint64_t few[kLpRanked], cta_list[32];
+    __shared__ int found, ranked;
     constexpr int VEC = RowView<T>::VEC;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
     const uint32_t rank = cluster_ctarank(), ctas = cluster_nctarank();
@@ -338,19 +343,71 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) logprobs_kernel(const 
         }
     };
 
-    if (a.n_top && threadIdx.x < 4) chunk_max[chunks + threadIdx.x] = 0u;
+    // For the top list each of the first `voters` warps publishes its j-th best lane maximum so
+    // far, voters * j >= n: the lowest of them is a bound that n logits reach.  (A warp with a
+    // single chunk that does not fill its lanes stands aside if others can.)
+    const int n = TOP ? a.n_top : 0;
+    int voters = min(warps, chunks);
+    if (voters > 1 && chunks <= warps && (g_first + chunks - 1) * kLpChunk + 31 >= row.nvec) --voters;
+    float lane_top = -INFINITY;
+    auto publish = [&]() {
+        if (warp >= voters) {
+            if (lane == 0) vote[warp] = 0xFFFFFFFFu;
+            return;
+        }
+        uint32_t key = (g_first + warp) * kLpChunk + lane < row.nvec ? order_of(lane_top) : 0u;
+        uint32_t nth = 0u;
+        for (int i = 0; i < n; i += voters) {
+            nth = __reduce_max_sync(0xffffffffu, key);
+            if (lane == __ffs(__ballot_sync(0xffffffffu, key == nth)) - 1) key = 0u;
+        }
+        if (lane == 0) vote[warp] = nth;
+    };
+    auto lowest_vote = [&]() {
+        return __reduce_min_sync(0xffffffffu, lane < voters ? *(volatile uint32_t*)&vote[lane] : 0xFFFFFFFFu);
+    };
+    if (TOP && threadIdx.x == 0) found = 0, ranked = 0;
+    int round = 0;
+    bool all = true;                                         // no bound yet
+    float bound = -INFINITY;
     RowSums sums;
     sums.init();
-    for (int g = warp; g < chunks; g += warps) {
+    for (int g = warp; g < chunks; g += warps, ++round) {
         uint4 q[kLpUnroll];
         load_chunk(g, q);
-        const float top = lane_max<T>(q);
-        if (a.n_top) {
-            const uint32_t o = __reduce_max_sync(0xffffffffu, max(order_of(top), 1u));
-            if (lane == 0) chunk_max[g] = o;
+        float mx[kLpUnroll], top;
+#pragma unroll
+        for (int u = 0; u < kLpUnroll; ++u) {
+            mx[u] = vector_max<T>(q[u]);
+            top = u ? fmaxf(top, mx[u]) : mx[u];
+        }
+        if constexpr (TOP) {
+            lane_top = fmaxf(lane_top, top);
+            if ((round & (round - 1)) == 0) {                // a new bound in rounds 0, 1, 2, 4, 8, ...
+                publish();
+                if (round == 0) __syncthreads();
+                else __syncwarp();
+                const uint32_t lowest = lowest_vote();
+                all = lowest == 0u;
+                bound = value_of(lowest);
+            }
+            if (__any_sync(0xffffffffu, all || top >= bound)) {
+#pragma unroll
+                for (int u = 0; u < kLpUnroll; ++u) {
+                    const int v = (g_first + g) * kLpChunk + u * 32 + lane;
+                    if (v < row.nvec && (all || mx[u] >= bound)) {
+                        const int at = atomicAdd(&found, 1);
+                        if (at < kLpAside) aside[at] = q[u], aside_v[at] = v;
+                    }
+                }
+            }
         }
         if (top > sums.m) sums.raise(top, c2);
         add_vectors<T>(q, c2, sums);
+    }
+    if constexpr (TOP) {
+        publish();                                           // read after the next barrier
+        if (round == 0) __syncthreads();                     // a warp without chunks: the others' first round
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -364,7 +421,7 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) logprobs_kernel(const 
     __syncthreads();
     sums.init();
     if (lane < warps) sums = warp_sums[lane];
-    for (int o = WARPS / 2; o; o >>= 1) {
+    for (int o = kLpMaxWarps / 2; o; o >>= 1) {
         RowSums other;
         other.m = __shfl_xor_sync(0xffffffffu, sums.m, o);
         other.s = __shfl_xor_sync(0xffffffffu, sums.s, o);
@@ -448,7 +505,7 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) logprobs_kernel(const 
             a.stats[2 * r + 1] = ls;
         }
     }
-    if (!a.n_top) {
+    if constexpr (!TOP) {
         if (ctas > 1) cluster_sync();                                // remote sums have been read
         return;
     }
@@ -477,7 +534,6 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) logprobs_kernel(const 
         list.merge_reversed(__shfl_sync(0xffffffffu, next.key, 31 - lane),
                             __shfl_sync(0xffffffffu, next.idx, 31 - lane));
     };
-    const int n = a.n_top;
     auto write_top = [&](int i, uint32_t key, uint32_t idx) {
         a.top_idx[r * n + i] = (int32_t)idx;
         a.top_logp[r * n + i] = logp_of(value_of(key));
@@ -487,71 +543,41 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) logprobs_kernel(const 
         if (ctas > 1) cta_list[i] = pack_entry(key, idx);
         else write_top(i, key, idx);
     };
-    bool sorted = true;                                      // by the general way below
-    if (chunks >= n && chunks <= kLpRanked) {
-        // The usual way: every chunk's place by comparing it with all others ...
-        for (int g = threadIdx.x; g < chunks; g += blockDim.x) {
-            const uint32_t key = chunk_max[g];
-            int place = 0;
-#pragma unroll 4
-            for (int o = 0; o < (chunks + 3) / 4; ++o) {     // (the array is zeros up to a multiple of four)
-                const uint4 k = reinterpret_cast<const uint4*>(chunk_max)[o];
-                place += k.x >= key + (4 * o >= g);
-                place += k.y >= key + (4 * o + 1 >= g);
-                place += k.z >= key + (4 * o + 2 >= g);
-                place += k.w >= key + (4 * o + 3 >= g);
-            }
-            if (place < n) sel[place] = g;
-            if (place == n - 1) least = key;                 // no logit below this is needed
-        }
-        if (threadIdx.x == 0) found = 0;
-        __syncthreads();
-        // ... then the logits of the n best that reach the n-th best maximum, in any order ...
-        const uint32_t bound = least;
-        for (int i0 = warp; i0 < n * kLpUnroll; i0 += kLpUnroll * warps) {
-            uint4 q[kLpUnroll];
-            int v[kLpUnroll];
-#pragma unroll
-            for (int u = 0; u < kLpUnroll; ++u) {
-                const int i = i0 + u * warps;
-                v[u] = i < n * kLpUnroll
-                           ? (g_first + (int)sel[i / kLpUnroll]) * kLpChunk + i % kLpUnroll * 32 + lane : row.nvec;
-                if (v[u] < row.nvec) q[u] = row.load(v[u], -INFINITY);
-            }
-#pragma unroll
-            for (int u = 0; u < kLpUnroll; ++u) {
-                if (v[u] >= row.nvec) continue;
-                float x[VEC];
-                RowView<T>::unpack(q[u], x);
-                float mx = x[0];
-#pragma unroll
-                for (int e = 1; e < VEC; ++e) mx = fmaxf(mx, x[e]);
-                if (max(order_of(mx), 1u) < bound) continue;
-                if (*(volatile int*)&found > kLpCandidates) continue;       // too many already
-                const int j0 = row.first(v[u]);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const uint32_t key = order_of(x[e]);
-                    if (j0 + e < 0 || j0 + e >= a.V || max(key, 1u) < bound) continue;
-                    const int at = atomicAdd(&found, 1);
-                    if (at < kLpCandidates) candidates[at] = pack_entry(key, (uint32_t)(j0 + e));
-                }
-            }
+    bool general = true;
+    const int elements = chunks ? min(a.V, row.first((g_first + chunks) * kLpChunk)) - max(0, row.first(g_first * kLpChunk)) : 0;
+    if (found <= kLpAside) {
+        // of the vectors set aside the logits that reach the last bound, and their places by
+        // comparing all of them
+        const uint32_t lowest = lowest_vote();
+        const float last = value_of(lowest);
+        for (int i = threadIdx.x; i < found * VEC; i += blockDim.x) {
+            const float x = to_f32<T>(reinterpret_cast<const T*>(aside)[i]);
+            const int j = row.first(aside_v[i / VEC]) + i % VEC;
+            if (j < 0 || j >= a.V || !(lowest == 0u || x >= last)) continue;
+            const int at = atomicAdd(&ranked, 1);
+            if (at < kLpRanked) few[at] = pack_entry(order_of(x), (uint32_t)j);
         }
         __syncthreads();
-        // ... and their places the same way.  Many equal logits: the general way.
-        if (found <= kLpCandidates) {
-            sorted = false;
-            for (int i = threadIdx.x; i < found; i += blockDim.x) {
-                const uint64_t own = candidates[i];
+        if (ranked <= kLpRanked && ranked >= min(n, elements)) {
+            general = false;
+            for (int i = threadIdx.x; i < ranked; i += blockDim.x) {
+                const uint64_t own = few[i];
                 int place = 0;
-                for (int o = 0; o < found; ++o) place += candidates[o] > own;
+                for (int o = 0; o < ranked; ++o) place += few[o] > own;
                 if (place < n) put(place, (uint32_t)(own >> 32), ~(uint32_t)own);
             }
+            for (int i = ranked + threadIdx.x; i < n; i += blockDim.x) put(i, 0u, kNone);
         }
     }
-    if (sorted) {
+    if (general) {
         // The general way, whose work does not depend on the logits: the n best chunks ...
+        for (int g = warp; g < chunks; g += warps) {
+            uint4 q[kLpUnroll];
+            load_chunk(g, q);
+            const uint32_t o = __reduce_max_sync(0xffffffffu, max(order_of(lane_max<T>(q)), 1u));
+            if (lane == 0) chunk_max[g] = o;
+        }
+        __syncthreads();
         WarpList list;
         list.init();
         for (int g = warp * 32; g < chunks; g += warps * 32)
@@ -596,14 +622,14 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) logprobs_kernel(const 
         // the CTAs' lists, n entries each, by comparing all of them
         cluster_sync();
         if (rank == 0) {
-            const int all = n * (int)ctas;                   // <= kLpCandidates
+            const int all = n * (int)ctas;                   // <= kLpRanked
             for (int i = threadIdx.x; i < all; i += blockDim.x)
-                candidates[i] = ld_cluster_u64(&cta_list[i % n], i / n);
+                few[i] = ld_cluster_u64(&cta_list[i % n], i / n);
             __syncthreads();
             for (int i = threadIdx.x; i < all; i += blockDim.x) {
-                const uint64_t own = candidates[i];
+                const uint64_t own = few[i];
                 int place = 0;
-                for (int o = 0; o < all; ++o) place += candidates[o] > own;
+                for (int o = 0; o < all; ++o) place += few[o] > own;
                 if (place < n && own != pack_entry(0u, kNone)) write_top(place, (uint32_t)(own >> 32), ~(uint32_t)own);
             }
         }
@@ -611,10 +637,9 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) logprobs_kernel(const 
     }
 }
 
-template <typename T>
-static auto pick_logprobs(int id_bytes, bool wide) -> void (*)(LogprobArgs) {
-    if (wide) return id_bytes == 8 ? logprobs_kernel<T, int64_t, 32> : logprobs_kernel<T, int32_t, 32>;
-    return id_bytes == 8 ? logprobs_kernel<T, int64_t, 8> : logprobs_kernel<T, int32_t, 8>;
+template <typename T, bool TOP>
+static auto pick_logprobs(int id_bytes) -> void (*)(LogprobArgs) {
+    return id_bytes == 8 ? logprobs_kernel<T, int64_t, TOP> : logprobs_kernel<T, int32_t, TOP>;
 }
 
 cudaError_t launch_token_logprobs(const LogprobCall& c, cudaStream_t stream) {
@@ -623,16 +648,21 @@ cudaError_t launch_token_logprobs(const LogprobCall& c, cudaStream_t stream) {
                   c.entropy, c.stats, c.n_top, c.top_idx, c.top_logp, c.ws};
     const int64_t vec = 16 / (int64_t)dtype_bytes(c.dtype);
     const int64_t chunks = (c.V + 2 * vec - 2) / (vec * kLpChunk) + 1;         // at most, at any alignment
-    // One warp per chunk, up to eight.  While there are SMs to spare a row is spread over a
-    // cluster, and where even that leaves most of them idle its CTAs have up to 32 warps.
+    // Eight warps per row, in a cluster of CTAs while there are SMs to spare (T = 64, 128000 FP32,
+    // n = 5: 16.5 us).  Many rows: four warps, so that twice as many rows are in flight and
+    // one row's end hides behind more others (8192 x 127901 BF16, n = 8: 345 against 372 us),
+    // unless that leaves the last wave of CTAs much emptier (T = 1300: 80 against 74 us).
+    const int64_t eights = 4 * (int64_t)c.num_sms, fours = 2 * eights;       // CTAs resident at once
+    const int64_t waves8 = (c.T + eights - 1) / eights, waves4 = (c.T + fours - 1) / fours;
+    const int most = c.T > eights && 2 * waves4 * 4 <= waves8 * 5 ? 4 : kLpMaxWarps;
     int warps = 1, ctas = 1;
-    while (warps < 8 && warps < chunks) warps *= 2;
-    while (ctas < kLpMaxCluster && chunks > (int64_t)warps * ctas && c.T * ctas * 2 <= 4 * (int64_t)c.num_sms) ctas *= 2;
-    const bool wide = ctas == kLpMaxCluster && c.T * ctas <= c.num_sms && chunks > 8 * ctas;
-    while (wide && warps < kLpMaxWarps && chunks > (int64_t)warps * ctas) warps *= 2;
-    const size_t smem = c.n_top ? sizeof(uint32_t) * (size_t)((chunks + ctas - 1) / ctas + 4) : 0;
-    void (*k)(LogprobArgs) = c.dtype == MOE_F32 ? pick_logprobs<float>(c.id_bytes, wide)
-                                                : pick_logprobs<uint16_t>(c.id_bytes, wide);
+    while (warps < most && warps < chunks) warps *= 2;
+    while (ctas < kLpMaxCluster && chunks > (int64_t)warps * ctas && c.T * ctas * 2 <= eights) ctas *= 2;
+    const size_t smem = c.n_top ? sizeof(uint32_t) * (size_t)((chunks + ctas - 1) / ctas) : 0;
+    void (*k)(LogprobArgs) =
+        c.n_top ? (c.dtype == MOE_F32 ? pick_logprobs<float, true>(c.id_bytes) : pick_logprobs<uint16_t, true>(c.id_bytes))
+                : (c.dtype == MOE_F32 ? pick_logprobs<float, false>(c.id_bytes)
+                                      : pick_logprobs<uint16_t, false>(c.id_bytes));
     cudaLaunchConfig_t cfg{};
     if (c.T * ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
     cfg.gridDim = dim3((unsigned)(c.T * ctas));
