@@ -470,6 +470,13 @@ __host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N, int sfa_id, int 
 }
 
 // --------------------------------------------------------------- vector memory ops
+// Asynchronous 16-byte copy global -> shared (both addresses 16-byte aligned), and the wait
+// for all of this thread's.
+__device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 __device__ __forceinline__ uint4 ld_nc_v4(const void* p) {
     uint4 v;
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"

@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kOrderThreads)
     uint16_t* counts = reinterpret_cast<uint16_t*>(cursor + range);
     constexpr int kSweep = kOrderThreads * kOrderIds;
     static_assert(kSweep <= kOrderList, "a sweep's own tokens fit the list");
-    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int tid = threadIdx.x, lane = tid % 32;
     const int v0 = (int)((int64_t)blockIdx.x * range);
     const int rows = (int)(V - v0 < range ? V - v0 : range);
     for (int i = tid; i < rows; i += kOrderThreads) cursor[i] = 0;
@@ -545,16 +545,15 @@ __global__ void __launch_bounds__(kJoinCols * kJoinParts * 32, 2)
         const int64_t c0 = ((item % groups) * kJoinCols + col) * 256;
         const int k = a.key[(range + 1) * a.places - 1];
         // equal ids are neighbours: the run covers the next ranges as long as they begin with
-        // it; the first that does not, by 32 looks at a time
-        int lo = range + 2, hi = a.ranges;                        // range + 1 begins with it
-        while (lo < hi) {
-            const int step = (hi - lo + 31) / 32;
+        // it; the first that does not, among the next 32 or, 32 looks at a time, all others
+        int lo = range + 1, hi = a.ranges;
+        for (int step = 1; lo < hi; step = (hi - lo + 31) / 32) {
             const int64_t r = lo + (int64_t)lane * step;
             const bool in = r < hi && r * a.places < live && a.key[r * a.places] == k;
             const int n = __popc(__ballot_sync(0xffffffffu, in));
+            if (n < 32) hi = min((int64_t)hi, lo + (int64_t)n * step);
             if (n == 0) break;
-            hi = min(hi, lo + n * step);
-            lo = lo + (n - 1) * step + 1;
+            lo += (n - 1) * step + 1;
         }
         const int rows = lo - range;                              // partial rows: [range][1], then [r][0]
         const int first = (int)((int64_t)rows * part / kJoinParts), last = (int)((int64_t)rows * (part + 1) / kJoinParts);

@@ -123,7 +123,7 @@ struct RowView {
     // the vector's elements; fill past the row
     __device__ uint4 load(int v, float fill) const {
         const int j = first(v);
-        if (whole(v)) return ld_nc_v4(p + j);
+        if (whole(v)) return ld_v4(p + j);
         T e[VEC];
 #pragma unroll
         for (int i = 0; i < VEC; ++i) e[i] = j + i >= 0 && j + i < V ? p[j + i] : from_f32<T>(fill);
@@ -195,7 +195,7 @@ constexpr int kLpMaxWarps = 8;
 constexpr int kLpUnroll = 4;                    // vectors a lane holds at once
 constexpr int kLpChunk = 32 * kLpUnroll;        // vectors a warp reads at once: one chunk
 constexpr int kLpMaxCluster = 8;
-constexpr int kLpAside = 512;                   // vectors set aside during the pass
+constexpr int kLpAside = 256;                   // vectors set aside during the pass
 constexpr int kLpRanked = 256;                  // logits whose places are found by comparing all of them
 static_assert(kLpMaxCluster * kMaxTop <= kLpRanked, "the CTAs' lists are ranked together");
 
@@ -308,7 +308,7 @@ __device__ __forceinline__ void add_vectors(const uint4 (&q)[kLpUnroll], float c
 // of its own; likewise in the n best vectors of these, which are 8 n (FP32: 4 n) logits.
 template <typename T, typename Id, bool TOP>
 __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __grid_constant__ LogprobArgs a) {
-    extern __shared__ uint32_t chunk_max[];                  // the general way's: order_of the maximum, at least 1
+    extern __shared__ __align__(16) uint8_t smem[];          // the chunks read ahead; later chunk_max
     __shared__ RowSums warp_sums[kLpMaxWarps], cta_sums;
     __shared__ CarefulSums warp_careful[kLpMaxWarps], cta_careful;
     __shared__ uint32_t vote[kLpMaxWarps], sel[32];
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
         const T* p = row.p + row.first(v0) + lane * VEC;
         if (row.whole(v0) && row.whole(v0 + kLpChunk - 1)) {         // the same for the whole warp
 #pragma unroll
-            for (int u = 0; u < kLpUnroll; ++u) q[u] = ld_nc_v4(p + u * 32 * VEC);
+            for (int u = 0; u < kLpUnroll; ++u) q[u] = ld_v4(p + u * 32 * VEC);
         } else {
             const uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;      // -inf
 #pragma unroll
@@ -342,11 +342,34 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
             }
         }
     };
+    // BF16 rows (twice the arithmetic per byte): the pass copies each warp's next chunk to shared
+    // memory while it works on this one, 335 against 345 us for 8192 x 127901 and n = 8; FP32 rows
+    // were up to 20% slower so.  Every lane copies and takes its own vectors: no barrier.
+    constexpr bool kAhead = sizeof(T) == 2;
+    uint4* ring = reinterpret_cast<uint4*>(smem) + warp * kLpUnroll * 32 + lane;
+    auto prefetch = [&](int g) {
+        const int v0 = (g_first + g) * kLpChunk;
+        if (g < chunks && row.whole(v0) && row.whole(v0 + kLpChunk - 1)) {
+            const T* p = row.p + row.first(v0) + lane * VEC;
+#pragma unroll
+            for (int u = 0; u < kLpUnroll; ++u) cp_async_16(ring + u * 32, p + u * 32 * VEC);
+        }
+    };
+    auto take_chunk = [&](int g, uint4 (&q)[kLpUnroll]) {
+        const int v0 = (g_first + g) * kLpChunk;
+        if (kAhead && row.whole(v0) && row.whole(v0 + kLpChunk - 1)) {
+            cp_async_wait_all();
+#pragma unroll
+            for (int u = 0; u < kLpUnroll; ++u) q[u] = ring[u * 32];
+        } else {
+            load_chunk(g, q);
+        }
+    };
 
     // For the top list each of the first `voters` warps publishes its j-th best lane maximum so
     // far, voters * j >= n: the lowest of them is a bound that n logits reach.  (A warp with a
     // single chunk that does not fill its lanes stands aside if others can.)
-    const int n = TOP ? a.n_top : 0;
+    const int n = a.n_top;
     int voters = min(warps, chunks);
     if (voters > 1 && chunks <= warps && (g_first + chunks - 1) * kLpChunk + 31 >= row.nvec) --voters;
     float lane_top = -INFINITY;
@@ -372,9 +395,11 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
     float bound = -INFINITY;
     RowSums sums;
     sums.init();
+    if (kAhead) prefetch(warp);
     for (int g = warp; g < chunks; g += warps, ++round) {
         uint4 q[kLpUnroll];
-        load_chunk(g, q);
+        take_chunk(g, q);
+        if (kAhead) prefetch(g + warps);
         float mx[kLpUnroll], top;
 #pragma unroll
         for (int u = 0; u < kLpUnroll; ++u) {
@@ -571,6 +596,7 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
     }
     if (general) {
         // The general way, whose work does not depend on the logits: the n best chunks ...
+        uint32_t* chunk_max = reinterpret_cast<uint32_t*>(smem);     // order_of the maximum, at least 1
         for (int g = warp; g < chunks; g += warps) {
             uint4 q[kLpUnroll];
             load_chunk(g, q);
@@ -658,7 +684,9 @@ cudaError_t launch_token_logprobs(const LogprobCall& c, cudaStream_t stream) {
     int warps = 1, ctas = 1;
     while (warps < most && warps < chunks) warps *= 2;
     while (ctas < kLpMaxCluster && chunks > (int64_t)warps * ctas && c.T * ctas * 2 <= eights) ctas *= 2;
-    const size_t smem = c.n_top ? sizeof(uint32_t) * (size_t)((chunks + ctas - 1) / ctas) : 0;
+    const size_t ahead = c.dtype == MOE_F32 ? 0 : (size_t)warps * kLpChunk * sizeof(uint4);
+    const size_t maxima = c.n_top ? sizeof(uint32_t) * (size_t)((chunks + ctas - 1) / ctas) : 0;
+    const size_t smem = ahead > maxima ? ahead : maxima;
     void (*k)(LogprobArgs) =
         c.n_top ? (c.dtype == MOE_F32 ? pick_logprobs<float, true>(c.id_bytes) : pick_logprobs<uint16_t, true>(c.id_bytes))
                 : (c.dtype == MOE_F32 ? pick_logprobs<float, false>(c.id_bytes)
