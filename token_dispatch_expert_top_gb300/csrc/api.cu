@@ -294,12 +294,12 @@ EmbedPlan make_embed_plan(int64_t N, int64_t V, int64_t H) {
         off += align256(bytes);
         return o;
     };
-    pl.n_live = take(2 * sizeof(int32_t));
-    pl.crossing = take(sizeof(int32_t) * (size_t)embed_ranges(N, H));
+    pl.n_live = take(3 * sizeof(int32_t));
+    pl.crossing = take(sizeof(int4) * (size_t)embed_ranges(N, H));
     pl.order = take(sizeof(int32_t) * (size_t)N);
     pl.key = take(sizeof(int32_t) * (size_t)N);
     pl.present = take(sizeof(uint32_t) * (size_t)((V + 31) / 32));
-    pl.part = take(sizeof(float) * 2 * (size_t)embed_ranges(N, H) * (size_t)((H + 7) / 8 * 8));
+    pl.part = take(sizeof(float) * 2 * (size_t)embed_ranges(N, H) * (size_t)((H + 255) / 256 * 256));
     pl.total = off;
     return pl;
 }
@@ -1107,7 +1107,7 @@ int moe_embedding_backward(const void* ids, int id_bytes, int64_t N, int64_t V, 
     c.order = at<int32_t>(workspace, pl.order);
     c.key = at<int32_t>(workspace, pl.key);
     c.n_live = at<int32_t>(workspace, pl.n_live);
-    c.crossing = at<int32_t>(workspace, pl.crossing);
+    c.crossing = at<int4>(workspace, pl.crossing);
     c.present = at<uint32_t>(workspace, pl.present);
     c.part = at<float>(workspace, pl.part);
     c.num_sms = num_sms_current();

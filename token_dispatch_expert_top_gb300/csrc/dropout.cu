@@ -48,9 +48,10 @@ __device__ __forceinline__ bool kept(const uint32_t (&w)[4], int i, const Dropou
 // Aligned rows: one thread per group of eight columns (one counter), 16-byte accesses.  Each
 // thread does one group and ends: blocks that write in address order keep the DRAM writes
 // together (zeroing 3.7 GB: 7.8 TB/s so, 6.6 TB/s by a grid that strides over the data).
+constexpr int kDropThreads = 128;
 template <typename T>
-__global__ void __launch_bounds__(256) dropout_groups_kernel(const __grid_constant__ DropoutArgs a) {
-    const uint64_t b = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+__global__ void __launch_bounds__(kDropThreads) dropout_groups_kernel(const __grid_constant__ DropoutArgs a) {
+    const uint64_t b = (uint64_t)blockIdx.x * kDropThreads + threadIdx.x;
     uint64_t r = 0;
     if (a.rows == 1) {
         if (b >= (uint64_t)a.groups) return;
@@ -61,9 +62,8 @@ __global__ void __launch_bounds__(256) dropout_groups_kernel(const __grid_consta
     const int64_t c = (int64_t)(b - r * a.groups) * 8;
     float v[8], y[8];
     load8<T, true>((const T*)a.x + r * a.ld_x + c, 8, v);
-    if (a.residual) {
-        load8<T, true>((const T*)a.residual + r * a.ld_res + c, 8, y);
-    } else {
+    if (a.residual) load8<T, true>((const T*)a.residual + r * a.ld_res + c, 8, y);
+    if (!a.residual) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = 0.f;
     }
@@ -135,10 +135,10 @@ cudaError_t launch_dropout(const void* x, int dtype, int64_t rows, int64_t cols,
     }
     if (rows > (1ll << 60) / a.groups) return cudaErrorInvalidValue;
     if (vec) {
-        const int64_t grid = (rows * a.groups + 255) / 256;
+        const int64_t grid = (rows * a.groups + kDropThreads - 1) / kDropThreads;
         if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-        if (dtype == MOE_F32) dropout_groups_kernel<float><<<(unsigned)grid, 256, 0, stream>>>(a);
-        else dropout_groups_kernel<uint16_t><<<(unsigned)grid, 256, 0, stream>>>(a);
+        if (dtype == MOE_F32) dropout_groups_kernel<float><<<(unsigned)grid, kDropThreads, 0, stream>>>(a);
+        else dropout_groups_kernel<uint16_t><<<(unsigned)grid, kDropThreads, 0, stream>>>(a);
     } else {
         const int64_t chunks = (cols + 255) / 256;
         const int64_t grid = (rows * chunks + 7) / 8;

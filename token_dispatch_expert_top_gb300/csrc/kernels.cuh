@@ -234,10 +234,10 @@ struct EmbedBackward {
     int accumulate;
     int32_t* order;           // [N] scratch: tokens sorted by (id, token)
     int32_t* key;             // [N] scratch: their ids
-    int32_t* n_live;          // [2] scratch: how many have an id; runs that cross a range's end
-    int32_t* crossing;        // [ranges] scratch: where those runs begin
+    int32_t* n_live;          // [3] scratch: how many have an id; runs that cross a range's end
+    int4* crossing;           // [ranges] scratch: those runs
     uint32_t* present;        // [V / 32, rounded up] scratch: ids that a token names
-    float* part;              // [2 ranges][H rounded up to 8] scratch
+    float* part;              // [2 ranges][H rounded up to 256] scratch
     int num_sms;
     WsHeader* ws;
 };
