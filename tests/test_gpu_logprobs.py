@@ -171,6 +171,24 @@ def test_one_logit_left_is_certain(M, T, dtype):
         assert torch.equal(o["top_idx"][:, 0].long(), t) and not o["top_logp"][:, 0].any()
 
 
+@pytest.mark.parametrize("T", [3, 40, 700])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("left", [0, 1, 2, 7, 31, 33, 200])
+def test_few_logits_left(M, T, dtype, left):
+    """Grammar-masked rows: `left` logits, at the front, at the end, spread, in one run; the
+    masked ones fill the list by index."""
+    V = 9001
+    gen = torch.Generator(device="cuda").manual_seed(left)
+    full = _logits(T, V, dtype, seed=left)
+    x = torch.full((T, V), -INF, dtype=dtype, device="cuda")
+    for r in range(T):
+        at = (torch.arange(left, device="cuda"), V - 1 - torch.arange(left, device="cuda"),
+              torch.randperm(V, generator=gen, device="cuda")[:left], 4000 + torch.arange(left, device="cuda"))[r % 4]
+        x[r, at] = full[r, at]
+    for n in (1, 8, 32):
+        _check(M, x, _targets(T, V).int(), 1.0, n, grad=T < 10)
+
+
 def test_extreme_values(M):
     """Logits of up to the largest finite values, both signs; probabilities that underflow."""
     x = torch.zeros((4, 600), device="cuda")

@@ -195,7 +195,7 @@ constexpr int kLpMaxWarps = 8;
 constexpr int kLpUnroll = 4;                    // vectors a lane holds at once
 constexpr int kLpChunk = 32 * kLpUnroll;        // vectors a warp reads at once: one chunk
 constexpr int kLpMaxCluster = 8;
-constexpr int kLpAside = 256;                   // vectors set aside during the pass
+constexpr int kLpAside = 512;                   // vectors set aside during the pass
 constexpr int kLpRanked = 256;                  // logits whose places are found by comparing all of them
 static_assert(kLpMaxCluster * kMaxTop <= kLpRanked, "the CTAs' lists are ranked together");
 
@@ -300,7 +300,8 @@ __device__ __forceinline__ void add_vectors(const uint4 (&q)[kLpUnroll], float c
 // an SM; per BF16 logit about 5 instructions are issued, of which one is the exponential.
 // For the top list the pass sets aside, from registers, the vectors with a logit that reaches a
 // bound which rises as it goes; about a hundred for n = 8, of which some 3 n logits reach the
-// last bound and are ranked.  (Reading the best chunks again afterwards cost a trip to DRAM per row, as the rows
+// last bound and are ranked.  Masked logits are never set aside; they fill the list's end by
+// index.  (Reading the best chunks again afterwards cost a trip to DRAM per row, as the rows
 // in flight do not fit L2: 369 against 345 us for 8192 x 127901 BF16 and n = 8.)  Where
 // the logits' order or ties make too many, a way whose work does not depend on the logits is
 // taken: the n best logits lie in the n best chunks (what a warp reads at once) by (maximum,
@@ -408,7 +409,8 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
         }
         if constexpr (TOP) {
             lane_top = fmaxf(lane_top, top);
-            if ((round & (round - 1)) == 0) {                // a new bound in rounds 0, 1, 2, 4, 8, ...
+            // a new bound in rounds 0, 1, 2, 4, 8, ...; for long lists in 3, 6, 12, ... too
+            if ((round & (round - 1)) == 0 || (n > 8 && round == 3 * (round & -round))) {
                 publish();
                 if (round == 0) __syncthreads();
                 else __syncwarp();
@@ -420,7 +422,7 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
 #pragma unroll
                 for (int u = 0; u < kLpUnroll; ++u) {
                     const int v = (g_first + g) * kLpChunk + u * 32 + lane;
-                    if (v < row.nvec && (all || mx[u] >= bound)) {
+                    if (v < row.nvec && mx[u] > -INFINITY && (all || mx[u] >= bound)) {
                         const int at = atomicAdd(&found, 1);
                         if (at < kLpAside) aside[at] = q[u], aside_v[at] = v;
                     }
@@ -569,21 +571,27 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
         else write_top(i, key, idx);
     };
     bool general = true;
-    const int elements = chunks ? min(a.V, row.first((g_first + chunks) * kLpChunk)) - max(0, row.first(g_first * kLpChunk)) : 0;
     if (found <= kLpAside) {
         // of the vectors set aside the logits that reach the last bound, and their places by
         // comparing all of them
-        const uint32_t lowest = lowest_vote();
+        const uint32_t lowest = lowest_vote(), masked = order_of(-INFINITY);
         const float last = value_of(lowest);
         for (int i = threadIdx.x; i < found * VEC; i += blockDim.x) {
             const float x = to_f32<T>(reinterpret_cast<const T*>(aside)[i]);
             const int j = row.first(aside_v[i / VEC]) + i % VEC;
-            if (j < 0 || j >= a.V || !(lowest == 0u || x >= last)) continue;
+            if (j < 0 || j >= a.V || !(x > -INFINITY) || !(lowest == 0u || x >= last)) continue;
             const int at = atomicAdd(&ranked, 1);
             if (at < kLpRanked) few[at] = pack_entry(order_of(x), (uint32_t)j);
         }
         __syncthreads();
-        if (ranked <= kLpRanked && ranked >= min(n, elements)) {
+        const int j0 = max(0, row.first(g_first * kLpChunk));        // this CTA's first logit
+        const int need = min(n, chunks ? min(a.V, row.first((g_first + chunks) * kLpChunk)) - j0 : 0);
+        // Fewer unmasked logits than places (they have all been set aside then): masked ones
+        // follow, the lowest indices, which are among the first `need`.
+        unsigned rest = 0u;
+        if (ranked < need && lowest <= masked)
+            rest = __ballot_sync(0xffffffffu, lane < need && to_f32<T>(row.p[j0 + lane]) == -INFINITY);
+        if (ranked <= kLpRanked && ranked + __popc(rest) >= need) {
             general = false;
             for (int i = threadIdx.x; i < ranked; i += blockDim.x) {
                 const uint64_t own = few[i];
@@ -591,7 +599,11 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
                 for (int o = 0; o < ranked; ++o) place += few[o] > own;
                 if (place < n) put(place, (uint32_t)(own >> 32), ~(uint32_t)own);
             }
-            for (int i = ranked + threadIdx.x; i < n; i += blockDim.x) put(i, 0u, kNone);
+            if (warp == 0) {
+                const int place = ranked + __popc(rest & ((1u << lane) - 1u));
+                if (rest >> lane & 1 && place < need) put(place, masked, (uint32_t)(j0 + lane));
+                if (lane >= need && lane < n) put(lane, 0u, kNone);
+            }
         }
     }
     if (general) {
@@ -674,8 +686,9 @@ cudaError_t launch_token_logprobs(const LogprobCall& c, cudaStream_t stream) {
                   c.entropy, c.stats, c.n_top, c.top_idx, c.top_logp, c.ws};
     const int64_t vec = 16 / (int64_t)dtype_bytes(c.dtype);
     const int64_t chunks = (c.V + 2 * vec - 2) / (vec * kLpChunk) + 1;         // at most, at any alignment
-    // Eight warps per row, in a cluster of CTAs while there are SMs to spare (T = 64, 128000 FP32,
-    // n = 5: 16.5 us).  Many rows: four warps, so that twice as many rows are in flight and
+    // Eight warps per row, in a cluster of CTAs while these fill at most 13/16 of the places (not
+    // every place takes a cluster: T = 150, 128000 FP32, n = 5: 25 us in 300 CTAs, 32 in 600;
+    // T = 64: 14.4 in 256, 16.4 in 512, 16 and more in 64).  Many rows: four warps, so that twice as many rows are in flight and
     // one row's end hides behind more others (8192 x 127901 BF16, n = 8: 345 against 372 us),
     // unless that leaves the last wave of CTAs much emptier (T = 1300: 80 against 74 us).
     const int64_t eights = 4 * (int64_t)c.num_sms, fours = 2 * eights;       // CTAs resident at once
@@ -683,7 +696,7 @@ cudaError_t launch_token_logprobs(const LogprobCall& c, cudaStream_t stream) {
     const int most = c.T > eights && 2 * waves4 * 4 <= waves8 * 5 ? 4 : kLpMaxWarps;
     int warps = 1, ctas = 1;
     while (warps < most && warps < chunks) warps *= 2;
-    while (ctas < kLpMaxCluster && chunks > (int64_t)warps * ctas && c.T * ctas * 2 <= eights) ctas *= 2;
+    while (ctas < kLpMaxCluster && chunks > (int64_t)warps * ctas && c.T * ctas * 2 <= eights * 13 / 16) ctas *= 2;
     const size_t ahead = c.dtype == MOE_F32 ? 0 : (size_t)warps * kLpChunk * sizeof(uint4);
     const size_t maxima = c.n_top ? sizeof(uint32_t) * (size_t)((chunks + ctas - 1) / ctas) : 0;
     const size_t smem = ahead > maxima ? ahead : maxima;
@@ -702,7 +715,7 @@ cudaError_t launch_token_logprobs(const LogprobCall& c, cudaStream_t stream) {
     at.val.clusterDim.x = ctas;
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = ctas > 1;
     return cudaLaunchKernelEx(&cfg, k, a);
 }
 

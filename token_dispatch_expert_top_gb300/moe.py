@@ -372,13 +372,15 @@ def _rows(fn: str, name: str, t: torch.Tensor) -> tuple[int, int, int, int, int]
         raise TypeError(f"{fn}: {name} is {t.dtype}; float32 or bfloat16 is wanted")
     if not t.is_cuda:
         raise ValueError(f"{fn}: {name} is not on a CUDA device")
-    if t.dim() != 2:
-        if t.dim() == 0:
+    shape = t.shape
+    if len(shape) != 2:
+        if not shape:
             raise ValueError(f"{fn}: {name} has no columns")
-        t = t.view(-1, t.shape[-1])
-    rows, cols = t.shape
-    ld = t.stride(0)
-    if cols > 1 and t.stride(1) != 1:
+        t = t.view(-1, shape[-1])
+        shape = t.shape
+    rows, cols = shape
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{fn}: the rows of {name} are not contiguous")
     return t.data_ptr(), dt, rows, cols, ld if rows > 1 else max(ld, cols)
 
