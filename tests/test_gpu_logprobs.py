@@ -291,6 +291,21 @@ def test_rows_past_32_bit_offsets(M):
     assert abs(float(x[0, 5]) * V + 1) < 2.0 ** -7
 
 
+@pytest.mark.parametrize("T", [2, 250])
+def test_the_largest_vocabulary(M, T):
+    """2^22 FP32 logits a row (their last chunk partial at an odd alignment): ties throughout,
+    so the top list is looked for the general way, with the most chunks it can have."""
+    V = 1 << 22
+    buf = torch.zeros(T * (V + 1) + 1, device="cuda")
+    x = buf[1:].view(T, V + 1)[:, :V]
+    x[:, V - 3] = 2.0
+    t = torch.full((T,), V - 3, device="cuda")
+    o = _forward(M, x, t, 1.0, 32)
+    lse = np.log(np.exp(2.0) + V - 1)
+    assert float((o["logp"] - (2.0 - lse)).abs().max()) < 2 * _eps(V) + 2.0 ** -18
+    assert bool((o["top_idx"] == torch.tensor([V - 3] + list(range(31)), device="cuda")).all())
+
+
 def test_same_bits_every_time(M):
     x, t = _logits(64, 40001, BF16, seed=12), _targets(64, 40001)
     a, b = _forward(M, x, t, 1.0, 8), _forward(M, x, t, 1.0, 8)

@@ -296,8 +296,10 @@ __device__ __forceinline__ void add_vectors(const uint4 (&q)[kLpUnroll], float c
 }
 
 // One cluster of CTAs per row (each takes a contiguous share of the row's chunks), one pass
-// over the row.  Bound by HBM: 8 loads of 16 bytes per lane are in flight at most, 32 warps
-// an SM; per BF16 logit about 5 instructions are issued, of which one is the exponential.
+// over the row: 8192 x 127901 BF16 in 305 us (6.9 TB/s), with the top 8 in 334 us.  The pass is
+// bound by HBM: up to 8 loads of 16 bytes per lane are in flight, 32 warps an SM, and per BF16
+// logit about 7 instructions are issued, one of them the exponential.  With the top list it
+// is the latency of each row's end that shows, which the other rows in flight do not hide.
 // For the top list the pass sets aside, from registers, the vectors with a logit that reaches a
 // bound which rises as it goes; about a hundred for n = 8, of which some 3 n logits reach the
 // last bound and are ranked.  Masked logits are never set aside; they fill the list's end by
@@ -328,6 +330,10 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
     const int g_first = (int)rank * share;
     const int chunks = max(0, min(share, row_chunks - g_first));     // this CTA's
     const float c2 = a.scale * kLog2e;
+    auto sync_cluster = [&]() {
+        __syncwarp();                                        // the barrier wants whole warps
+        cluster_sync();
+    };
     auto load_chunk = [&](int g, uint4 (&q)[kLpUnroll]) {
         const int v0 = (g_first + g) * kLpChunk;
         const T* p = row.p + row.first(v0) + lane * VEC;
@@ -344,7 +350,7 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
         }
     };
     // BF16 rows (twice the arithmetic per byte): the pass copies each warp's next chunk to shared
-    // memory while it works on this one, 335 against 345 us for 8192 x 127901 and n = 8; FP32 rows
+    // memory while it works on this one: 335 against 345 us for 8192 x 127901 and n = 8.  FP32 rows
     // were up to 20% slower so.  Every lane copies and takes its own vectors: no barrier.
     constexpr bool kAhead = sizeof(T) == 2;
     uint4* ring = reinterpret_cast<uint4*>(smem) + warp * kLpUnroll * 32 + lane;
@@ -461,7 +467,7 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
     sums.t = __shfl_sync(0xffffffffu, sums.t, 0);
     if (ctas > 1) {
         if (threadIdx.x == 0) cta_sums = sums;
-        cluster_sync();
+        sync_cluster();
         sums.init();
         for (uint32_t k = 0; k < ctas; ++k) {
             RowSums o;
@@ -499,7 +505,7 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
         for (int w = 1; w < warps; ++w) cs.merge(warp_careful[w], c2);
         if (ctas > 1) {
             if (threadIdx.x == 0) cta_careful = cs;
-            cluster_sync();
+            sync_cluster();
             cs.init();
             for (uint32_t k = 0; k < ctas; ++k) {
                 CarefulSums o;
@@ -516,6 +522,7 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
         ls = kLn2 * l2;
         entropy = kLn2 * (l2 - sums.t / sums.s);
     }
+    if (entropy < 0.f) entropy = 0.f;                                // by rounding; NaN stays
     const bool empty = ls == -INFINITY;
     auto logp_of = [&](float x) { return empty || x == -INFINITY ? -INFINITY : (x - m) * a.scale - ls; };
     if (rank == 0 && threadIdx.x == 0) {
@@ -533,7 +540,7 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
         }
     }
     if constexpr (!TOP) {
-        if (ctas > 1) cluster_sync();                                // remote sums have been read
+        if (ctas > 1) sync_cluster();                                // remote sums have been read
         return;
     }
 
@@ -658,7 +665,7 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
     }
     if (ctas > 1) {
         // the CTAs' lists, n entries each, by comparing all of them
-        cluster_sync();
+        sync_cluster();
         if (rank == 0) {
             const int all = n * (int)ctas;                   // <= kLpRanked
             for (int i = threadIdx.x; i < all; i += blockDim.x)
@@ -671,7 +678,7 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
                 if (place < n && own != pack_entry(0u, kNone)) write_top(place, (uint32_t)(own >> 32), ~(uint32_t)own);
             }
         }
-        cluster_sync();                                      // remote lists and sums have been read
+        sync_cluster();                                      // remote lists and sums have been read
     }
 }
 
@@ -687,10 +694,11 @@ cudaError_t launch_token_logprobs(const LogprobCall& c, cudaStream_t stream) {
     const int64_t vec = 16 / (int64_t)dtype_bytes(c.dtype);
     const int64_t chunks = (c.V + 2 * vec - 2) / (vec * kLpChunk) + 1;         // at most, at any alignment
     // Eight warps per row, in a cluster of CTAs while these fill at most 13/16 of the places (not
-    // every place takes a cluster: T = 150, 128000 FP32, n = 5: 25 us in 300 CTAs, 32 in 600;
-    // T = 64: 14.4 in 256, 16.4 in 512, 16 and more in 64).  Many rows: four warps, so that twice as many rows are in flight and
-    // one row's end hides behind more others (8192 x 127901 BF16, n = 8: 345 against 372 us),
-    // unless that leaves the last wave of CTAs much emptier (T = 1300: 80 against 74 us).
+    // every place takes a cluster; 128000 FP32, n = 5: 64 rows take 14.4 us in 256 CTAs and 16.4
+    // in 512, 150 rows 25 us in 300 CTAs and 32 in 600).  Many rows: four warps, so that twice
+    // as many rows are in flight and one row's end hides behind more others (8192 x 127901
+    // BF16, n = 8: 345 against 372 us), unless that leaves the last wave of CTAs much emptier
+    // (1300 rows: 80 against 74 us).
     const int64_t eights = 4 * (int64_t)c.num_sms, fours = 2 * eights;       // CTAs resident at once
     const int64_t waves8 = (c.T + eights - 1) / eights, waves4 = (c.T + fours - 1) / fours;
     const int most = c.T > eights && 2 * waves4 * 4 <= waves8 * 5 ? 4 : kLpMaxWarps;
@@ -723,9 +731,9 @@ cudaError_t launch_token_logprobs(const LogprobCall& c, cudaStream_t stream) {
 // d x_j = p_j (g1 + g2 lp_j) + 1[j = t] scale g_logp with g2 = -scale g_entropy and
 // g1 = -scale (g_logp + g_entropy entropy).  dlogits may be the logits' own buffer: a thread
 // reads its elements before it writes them.  The kernel moves each logit in and its
-// gradient out once and is to be HBM-bound, which leaves it about 20 instructions per BF16
-// logit: whole blocks of a row away from its ends and its target take a path without checks
-// (6 per logit).
+// gradient out once, HBM-bound: 4096 x 128000 BF16 in 294 us (7.1 TB/s, part of the logits still in
+// L2).  That leaves about 20 instructions per BF16 logit: whole blocks of a row away from its
+// ends and its target take a path without checks (with them it issued 21 and took 365 us).
 struct LogprobGradArgs {
     const void* logits;
     int64_t T;
