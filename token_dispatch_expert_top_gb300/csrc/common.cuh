@@ -337,25 +337,10 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
         : "memory");
 }
 
-// ------------------------------------------------- launches that overlap their predecessor
-// Waits until the kernel before this one in the stream has finished and its writes are
-// visible (for kernels launched with programmatic stream serialization; otherwise at once).
-__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// Lets such a kernel's blocks start, up to their wait, as soon as every block of this one has
-// come here.
-__device__ __forceinline__ void grid_dependents_launch() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 // ------------------------------------------------------------ cluster helpers
 __device__ __forceinline__ uint32_t cluster_ctarank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_nctarank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
 // Address of the same shared-memory location in CTA `rank` of this cluster.
@@ -470,13 +455,6 @@ __host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N, int sfa_id, int 
 }
 
 // --------------------------------------------------------------- vector memory ops
-// Asynchronous 16-byte copy global -> shared (both addresses 16-byte aligned), and the wait
-// for all of this thread's.
-__device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 __device__ __forceinline__ uint4 ld_nc_v4(const void* p) {
     uint4 v;
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"

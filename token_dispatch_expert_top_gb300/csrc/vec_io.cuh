@@ -1,12 +1,37 @@
-// vec_io.cuh -- groups of eight consecutive FP32 or BF16 elements as FP32 registers:
-// the unit in which the operators around the layer (embedding.cu, logprobs.cu,
-// dropout.cu) move rows.  VECTOR: the group is 16-byte aligned and whole (one 16-byte
+// vec_io.cuh -- shared by the operators around the layer (embedding.cu, logprobs.cu,
+// dropout.cu): a few instructions, and groups of eight consecutive FP32 or BF16 elements as
+// FP32 registers, the unit in which they move rows.  VECTOR: the group is 16-byte aligned and whole (one 16-byte
 // access for BF16, two for FP32); otherwise element by element, `n` of the eight.
 #pragma once
 
 #include "common.cuh"
 
 namespace moe {
+
+// ------------------------------------------------- launches that overlap their predecessor
+// Waits until the kernel before this one in the stream has finished and its writes are
+// visible (for kernels launched with programmatic stream serialization; otherwise at once).
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets such a kernel's blocks start, up to their wait, as soon as every block of this one has
+// come here.
+__device__ __forceinline__ void grid_dependents_launch() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// CTAs of this cluster (1 without one).
+__device__ __forceinline__ uint32_t cluster_nctarank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
+// ------------------------------------------------------------------------ rows
+// Asynchronous 16-byte copy global -> shared (both addresses 16-byte aligned), and the wait
+// for all of this thread's.
+__device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Element types by moe_dtype_t; BF16 travels as its 16 bits.
 template <typename T>
