@@ -195,9 +195,13 @@ constexpr int kLpMaxWarps = 8;
 constexpr int kLpUnroll = 4;                    // vectors a lane holds at once
 constexpr int kLpChunk = 32 * kLpUnroll;        // vectors a warp reads at once: one chunk
 constexpr int kLpMaxCluster = 8;
-constexpr int kLpAside = 512;                   // vectors set aside during the pass
+constexpr int kLpKept = 512;                    // groups of a CTA whose lanes' maxima are kept (32 KB)
+constexpr int kLpAhead = 2;                      // chunks read ahead
 constexpr int kLpRanked = 256;                  // logits whose places are found by comparing all of them
-static_assert(kLpMaxCluster * kMaxTop <= kLpRanked, "the CTAs' lists are ranked together");
+// dynamic shared memory at most: the CTAs' lists, BF16 chunks read ahead, and the kept maxima
+constexpr int kLpLists = kLpMaxCluster * kMaxTop * 8;
+constexpr int kLpMaxSmem = kLpLists + kLpAhead * kLpMaxWarps * kLpChunk * 16 + kLpKept * 64;
+static_assert(kLpMaxSmem >= kLpLists + 4 * (kMaxLogprobVocab / (4 * kLpChunk) + 2), "the general way's chunk maxima fit, too");
 
 struct LogprobArgs {
     const void* logits;
@@ -205,6 +209,7 @@ struct LogprobArgs {
     int64_t ld;
     float scale;
     int careful;                                // the scale is outside the fast sums' range
+    int keep;                                   // shared memory holds the lanes' maxima of the chunks
     const void* targets;
     float *logp, *entropy, *stats;
     int n_top;
@@ -236,94 +241,138 @@ __device__ __forceinline__ float ld_cluster_f32(const void* p, uint32_t rank) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(p), rank)) : "memory");
     return v;
 }
-__device__ __forceinline__ uint64_t ld_cluster_u64(const void* p, uint32_t rank) {
-    uint64_t v;
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(mapa_shared(smem_u32(p), rank)) : "memory");
-    return v;
+__device__ __forceinline__ void st_cluster_f32(void* p, uint32_t rank, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(p), rank)), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_u64(void* p, uint32_t rank, uint64_t v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa_shared(smem_u32(p), rank)), "l"(v) : "memory");
+}
+// Halves of a barrier that only says that the cluster's CTAs have started.
+__device__ __forceinline__ void cluster_started_arrive() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_started_wait() {
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
-// Largest logit of a vector (NaN ignored).
+// Largest logit of one vector, or of a lane's vectors (NaN where all are; otherwise ignored).
 template <typename T>
 __device__ __forceinline__ float vector_max(const uint4& q) {
     if constexpr (sizeof(T) == 2) {
-        const uint32_t none = 0xFF80FF80u;      // -inf, -inf
-        const uint32_t h = max_bf16x2(max_bf16x2(max_bf16x2(q.x, q.y), max_bf16x2(q.z, q.w)), none);
+        const uint32_t h = max_bf16x2(max_bf16x2(q.x, q.y), max_bf16x2(q.z, q.w));
         return fmaxf(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u));
     } else {
-        return fmaxf(fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)),
-                           fmaxf(__uint_as_float(q.z), __uint_as_float(q.w))), -INFINITY);
+        return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)),
+                     fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
     }
 }
 template <typename T>
 __device__ __forceinline__ float lane_max(const uint4 (&q)[kLpUnroll]) {
-    float m = vector_max<T>(q[0]);
-#pragma unroll
-    for (int u = 1; u < kLpUnroll; ++u) m = fmaxf(m, vector_max<T>(q[u]));
-    return m;
+    static_assert(kLpUnroll == 4, "");
+    if constexpr (sizeof(T) == 2) {
+        uint4 h;
+        h.x = max_bf16x2(max_bf16x2(q[0].x, q[1].x), max_bf16x2(q[2].x, q[3].x));
+        h.y = max_bf16x2(max_bf16x2(q[0].y, q[1].y), max_bf16x2(q[2].y, q[3].y));
+        h.z = max_bf16x2(max_bf16x2(q[0].z, q[1].z), max_bf16x2(q[2].z, q[3].z));
+        h.w = max_bf16x2(max_bf16x2(q[0].w, q[1].w), max_bf16x2(q[2].w, q[3].w));
+        return vector_max<T>(h);
+    } else {
+        return fmaxf(fmaxf(vector_max<T>(q[0]), vector_max<T>(q[1])), fmaxf(vector_max<T>(q[2]), vector_max<T>(q[3])));
+    }
 }
 
-// Adds 2^y and y 2^y of the lane's vectors.
-template <typename T>
-__device__ __forceinline__ void add_vectors(const uint4 (&q)[kLpUnroll], float c2, RowSums& sums) {
-    const F2 c = f2(c2, c2), r = f2(-sums.m, -sums.m);
-    F2 s[2] = {f2(sums.s, 0.f), f2(0.f, 0.f)}, t[2] = {f2(sums.t, 0.f), f2(0.f, 0.f)};
+// A lane's running sums, RowSums' as four partial ones each.
+struct LaneSums {
+    float m;
+    F2 s[2], t[2];
+    __device__ void init() {
+        m = kFloor;
+        s[0] = s[1] = t[0] = t[1] = f2(0.f, 0.f);
+    }
+    __device__ void raise(float m2, float c2) {
+        const float d = (m - m2) * c2, f = exp2_approx(d);
 #pragma unroll
-    for (int u = 0; u < kLpUnroll; ++u) {
-        const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
-        constexpr int P = sizeof(T) == 2 ? 4 : 2;
+        for (int i = 0; i < 2; ++i) {
+            t[i] = f2_mul(f2(f, f), f2_fma(f2(d, d), s[i], t[i]));
+            s[i] = f2_mul(f2(f, f), s[i]);
+        }
+        m = m2;
+    }
+    // Adds 2^y and y 2^y of the lane's vectors.
+    template <typename T>
+    __device__ void add(const uint4 (&q)[kLpUnroll], float c2) {
+        const F2 c = f2(c2, c2), r = f2(-m, -m);
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-            F2 x;
-            if constexpr (sizeof(T) == 2) {
-                const uint32_t h = floor_bf16x2(w[p]);
-                x = f2(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u));
-            } else {
-                x = f2(floor_f32(__uint_as_float(w[2 * p])), floor_f32(__uint_as_float(w[2 * p + 1])));
+        for (int u = 0; u < kLpUnroll; ++u) {
+            const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+            constexpr int P = sizeof(T) == 2 ? 4 : 2;
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                F2 x;
+                if constexpr (sizeof(T) == 2) {
+                    const uint32_t h = floor_bf16x2(w[p]);
+                    x = f2(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u));
+                } else {
+                    x = f2(floor_f32(__uint_as_float(w[2 * p])), floor_f32(__uint_as_float(w[2 * p + 1])));
+                }
+                const F2 y = f2_mul(f2_add(x, r), c);
+                float y0, y1;
+                f2_split(y, y0, y1);
+                const F2 e = f2(exp2_approx(y0), exp2_approx(y1));
+                s[p & 1] = f2_add(s[p & 1], e);
+                t[p & 1] = f2_fma(e, y, t[p & 1]);
             }
-            const F2 y = f2_mul(f2_add(x, r), c);
-            float y0, y1;
-            f2_split(y, y0, y1);
-            const F2 e = f2(exp2_approx(y0), exp2_approx(y1));
-            s[p & 1] = f2_add(s[p & 1], e);
-            t[p & 1] = f2_fma(e, y, t[p & 1]);
         }
     }
-    float a, b;
-    f2_split(f2_add(s[0], s[1]), a, b);
-    sums.s = a + b;
-    f2_split(f2_add(t[0], t[1]), a, b);
-    sums.t = a + b;
-}
+    __device__ RowSums total() const {
+        RowSums o;
+        float a, b;
+        o.m = m;
+        f2_split(f2_add(s[0], s[1]), a, b);
+        o.s = a + b;
+        f2_split(f2_add(t[0], t[1]), a, b);
+        o.t = a + b;
+        return o;
+    }
+};
 
 // One cluster of CTAs per row (each takes a contiguous share of the row's chunks), one pass
-// over the row: 8192 x 127901 BF16 in 305 us (6.9 TB/s), with the top 8 in 334 us.  The pass is
-// bound by HBM: up to 8 loads of 16 bytes per lane are in flight, 32 warps an SM, and per BF16
+// over the row: 8192 x 127901 BF16 in 299 us (7.0 TB/s), with the top 8 in 318 us.  The pass is
+// bound by HBM: 8 copies of 16 bytes per lane are in flight, 32 warps an SM, and per BF16
 // logit about 7 instructions are issued, one of them the exponential.  With the top list it
 // is the latency of each row's end that shows, which the other rows in flight do not hide.
-// For the top list the pass sets aside, from registers, the vectors with a logit that reaches a
-// bound which rises as it goes; about a hundred for n = 8, of which some 3 n logits reach the
-// last bound and are ranked.  Masked logits are never set aside; they fill the list's end by
-// index.  (Reading the best chunks again afterwards cost a trip to DRAM per row, as the rows
-// in flight do not fit L2: 369 against 345 us for 8192 x 127901 BF16 and n = 8.)  Where
-// the logits' order or ties make too many, a way whose work does not depend on the logits is
-// taken: the n best logits lie in the n best chunks (what a warp reads at once) by (maximum,
-// position), as a chunk below those has n chunks before it, each with a logit that beats all
-// of its own; likewise in the n best vectors of these, which are 8 n (FP32: 4 n) logits.
-template <typename T, typename Id, bool TOP>
+// For the top list the pass only keeps the lanes' maxima of one or two chunks (a chunk is what
+// a warp reads at once), in 16 bits.  Afterwards they give a bound that the n best logits reach
+// and tell which lanes' shares of chunks hold such logits, some 3 n; these are read again, all
+// at once, and their logits that reach the bound are ranked.  (Noting logits during the pass,
+// against a bound that rises, cost 12200 warp instructions a row of 128000; this costs 7100
+// beside the pass's 29100.)  In a cluster the warps write their sums, and the CTAs their lists,
+// into the shared memory of those that want them, so that a row ends with one barrier of the
+// cluster: one row of 128000 FP32, n = 20, takes 9.9 us, 64 of 50001 BF16, n = 5, 10.2.  Masked logits
+// never count; they fill the list's end by index.  Where the logits' order or ties leave too
+// many, a way whose work does not depend on the logits is taken: the n best logits lie in the
+// n best chunks by (maximum, position), as a chunk below those has n chunks before it, each
+// with a logit that beats all of its own; likewise in the n best vectors of these, which are
+// 8 n (FP32: 4 n) logits.
+template <typename T, typename Id, bool TOP, bool CLUSTER>
 __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __grid_constant__ LogprobArgs a) {
-    extern __shared__ __align__(16) uint8_t smem[];          // the chunks read ahead; later chunk_max
-    __shared__ RowSums warp_sums[kLpMaxWarps], cta_sums;
+    // lists; the chunks read ahead; later chunk_max.  (Copies to shared memory that are not aligned
+    // to its lines of 128 bytes fetch their sectors twice: 340 instead of 316 us.)
+    extern __shared__ __align__(128) uint8_t dynamic_smem[];
+    __shared__ RowSums warp_sums[kLpMaxWarps * kLpMaxCluster];
     __shared__ CarefulSums warp_careful[kLpMaxWarps], cta_careful;
     __shared__ uint32_t vote[kLpMaxWarps], sel[32];
     __shared__ uint32_t list_key[kLpMaxWarps][32], list_idx[kLpMaxWarps][32];
-    __shared__ uint4 aside[kLpAside];
-    __shared__ int aside_v[kLpAside];
-    __shared__ uint64_t few[kLpRanked], cta_list[32];
-    __shared__ int found, ranked;
+    __shared__ uint32_t again[kLpRanked];
+    __shared__ uint64_t few[kLpRanked];
+    __shared__ int reached, ranked;
     constexpr int VEC = RowView<T>::VEC;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
-    const uint32_t rank = cluster_ctarank(), ctas = cluster_nctarank();
+    const uint32_t rank = CLUSTER ? cluster_ctarank() : 0, ctas = CLUSTER ? cluster_nctarank() : 1;
     const int64_t r = blockIdx.x / ctas;
+    if (CLUSTER) cluster_started_arrive();
+    uint64_t* lists = reinterpret_cast<uint64_t*>(dynamic_smem);     // the CTAs', n entries each, in the first
+    uint8_t* smem = dynamic_smem + (TOP ? ctas * kMaxTop * sizeof(uint64_t) : 0);
     const RowView<T> row((const T*)a.logits + r * a.ld, a.V);
     const int row_chunks = (row.nvec + kLpChunk - 1) / kLpChunk;
     const int share = (row_chunks + (int)ctas - 1) / (int)ctas;
@@ -334,57 +383,89 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
         __syncwarp();                                        // the barrier wants whole warps
         cluster_sync();
     };
+    // this CTA's chunks of whole vectors: all but the row's first and last, at most
+    const int whole_from = g_first == 0 && !row.whole(0) ? 1 : 0;
+    const int whole_to = row.whole((g_first + chunks) * kLpChunk - 1) ? chunks : chunks - 1;
+    const T* lane_row = row.p + row.first(g_first * kLpChunk) + lane * VEC;
+    auto load_partial = [&](int g, uint4 (&q)[kLpUnroll]) {
+        const uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;      // -inf
+#pragma unroll
+        for (int u = 0; u < kLpUnroll; ++u) {
+            const int v = (g_first + g) * kLpChunk + u * 32 + lane;
+            q[u] = v < row.nvec ? row.load(v, -INFINITY) : make_uint4(none, none, none, none);
+        }
+    };
+    auto whole = [&](int g) { return g >= whole_from && g < whole_to; };       // the same for the whole warp
     auto load_chunk = [&](int g, uint4 (&q)[kLpUnroll]) {
-        const int v0 = (g_first + g) * kLpChunk;
-        const T* p = row.p + row.first(v0) + lane * VEC;
-        if (row.whole(v0) && row.whole(v0 + kLpChunk - 1)) {         // the same for the whole warp
+        if (!whole(g)) return load_partial(g, q);
+        const T* p = lane_row + g * (kLpChunk * VEC);
 #pragma unroll
-            for (int u = 0; u < kLpUnroll; ++u) q[u] = ld_v4(p + u * 32 * VEC);
-        } else {
-            const uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;      // -inf
-#pragma unroll
-            for (int u = 0; u < kLpUnroll; ++u) {
-                const int v = v0 + u * 32 + lane;
-                q[u] = v < row.nvec ? row.load(v, -INFINITY) : make_uint4(none, none, none, none);
-            }
-        }
+        for (int u = 0; u < kLpUnroll; ++u) q[u] = ld_v4(p + u * 32 * VEC);
     };
-    // BF16 rows (twice the arithmetic per byte): the pass copies each warp's next chunk to shared
-    // memory while it works on this one: 335 against 345 us for 8192 x 127901 and n = 8.  FP32 rows
-    // were up to 20% slower so.  Every lane copies and takes its own vectors: no barrier.
-    constexpr bool kAhead = sizeof(T) == 2;
-    uint4* ring = reinterpret_cast<uint4*>(smem) + warp * kLpUnroll * 32 + lane;
-    auto prefetch = [&](int g) {
-        const int v0 = (g_first + g) * kLpChunk;
-        if (g < chunks && row.whole(v0) && row.whole(v0 + kLpChunk - 1)) {
-            const T* p = row.p + row.first(v0) + lane * VEC;
+    // The pass copies each warp's next two chunks to shared memory while it works on one; every
+    // lane copies and takes its own vectors: no barrier.  With n = 8, 4096 x 128000 FP32 take 301
+    // us so and 319 with plain loads, 700 rows 60 and 67; one chunk ahead is enough for neither
+    // type (8192 x 127901 BF16: 323 against 312 us).
+    uint4* ring = reinterpret_cast<uint4*>(smem) + warp * kLpAhead * kLpChunk + lane;
+    auto prefetch = [&](int g, int slot) {
+        if (whole(g)) {
+            const T* p = lane_row + g * (kLpChunk * VEC);
 #pragma unroll
-            for (int u = 0; u < kLpUnroll; ++u) cp_async_16(ring + u * 32, p + u * 32 * VEC);
+            for (int u = 0; u < kLpUnroll; ++u) cp_async_16(ring + slot * kLpChunk + u * 32, p + u * 32 * VEC);
         }
+        cp_async_commit();
     };
-    auto take_chunk = [&](int g, uint4 (&q)[kLpUnroll]) {
-        const int v0 = (g_first + g) * kLpChunk;
-        if (kAhead && row.whole(v0) && row.whole(v0 + kLpChunk - 1)) {
-            cp_async_wait_all();
-#pragma unroll
-            for (int u = 0; u < kLpUnroll; ++u) q[u] = ring[u * 32];
+    auto take_chunk = [&](int g, int slot, uint4 (&q)[kLpUnroll]) {
+        if (!whole(g)) {
+            load_partial(g, q);
         } else {
-            load_chunk(g, q);
+            cp_async_wait<kLpAhead - 1>();
+#pragma unroll
+            for (int u = 0; u < kLpUnroll; ++u) q[u] = ring[slot * kLpChunk + u * 32];
         }
     };
 
-    // For the top list each of the first `voters` warps publishes its j-th best lane maximum so
-    // far, voters * j >= n: the lowest of them is a bound that n logits reach.  (A warp with a
-    // single chunk that does not fill its lanes stands aside if others can.)
+    // For the top list: the upper half of the lanes' maxima of every kGroup chunks of a warp: of
+    // every two, which leaves the copies more shared memory (8192 rows: 4 us less), or in a
+    // cluster of every one, as then less is read again (64 x 50001 BF16: 0.7 us less).
     const int n = a.n_top;
+    constexpr int kGroup = CLUSTER ? 1 : 2;
+    uint16_t* kept = reinterpret_cast<uint16_t*>(smem + kLpAhead * warps * kLpChunk * sizeof(uint4));
+    const bool keep = a.keep;                                // room for them, in every CTA of the launch
+    float lane_top = -INFINITY, group_top = -INFINITY;
+    int round = 0, slot = 0;
+    if (TOP && threadIdx.x == 0) reached = ranked = 0;
+    LaneSums lane_sums;
+    lane_sums.init();
+    const bool first = rank == 0 && threadIdx.x == 0;
+    Id target = (Id)-1;
+    T target_logit = 0;
+    if (first && a.targets) target = ((const Id*)a.targets)[r];
+#pragma unroll
+    for (int d = 0; d < kLpAhead; ++d) prefetch(warp + d * warps, d);
+    for (int g = warp; g < chunks; g += warps) {
+        uint4 q[kLpUnroll];
+        take_chunk(g, slot, q);
+        prefetch(g + kLpAhead * warps, slot);
+        slot = slot + 1 == kLpAhead ? 0 : slot + 1;
+        const float top = lane_max<T>(q);
+        if constexpr (TOP) {
+            lane_top = fmaxf(lane_top, top);
+            group_top = kGroup > 1 && round % kGroup ? fmaxf(group_top, top) : top;
+            if (keep) kept[(round / kGroup * warps + warp) * 32 + lane] = (uint16_t)(__float_as_uint(group_top) >> 16);
+            ++round;
+        }
+        if (top > lane_sums.m) lane_sums.raise(top, c2);
+        lane_sums.template add<T>(q, c2);
+    }
+    if (target >= 0 && (int64_t)target < a.V) target_logit = row.p[target];
+    RowSums sums = lane_sums.total();
+    // Each of the first `voters` warps casts its j-th best lane maximum, voters * j >= n: the lowest
+    // of these votes is a bound that n logits reach.  (A warp with a single chunk that does not
+    // fill its lanes stands aside if others can vote.)
     int voters = min(warps, chunks);
     if (voters > 1 && chunks <= warps && (g_first + chunks - 1) * kLpChunk + 31 >= row.nvec) --voters;
-    float lane_top = -INFINITY;
-    auto publish = [&]() {
-        if (warp >= voters) {
-            if (lane == 0) vote[warp] = 0xFFFFFFFFu;
-            return;
-        }
+    if (TOP && warp < voters) {
         uint32_t key = (g_first + warp) * kLpChunk + lane < row.nvec ? order_of(lane_top) : 0u;
         uint32_t nth = 0u;
         for (int i = 0; i < n; i += voters) {
@@ -392,55 +473,6 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
             if (lane == __ffs(__ballot_sync(0xffffffffu, key == nth)) - 1) key = 0u;
         }
         if (lane == 0) vote[warp] = nth;
-    };
-    auto lowest_vote = [&]() {
-        return __reduce_min_sync(0xffffffffu, lane < voters ? *(volatile uint32_t*)&vote[lane] : 0xFFFFFFFFu);
-    };
-    if (TOP && threadIdx.x == 0) found = 0, ranked = 0;
-    int round = 0;
-    bool all = true;                                         // no bound yet
-    float bound = -INFINITY;
-    RowSums sums;
-    sums.init();
-    if (kAhead) prefetch(warp);
-    for (int g = warp; g < chunks; g += warps, ++round) {
-        uint4 q[kLpUnroll];
-        take_chunk(g, q);
-        if (kAhead) prefetch(g + warps);
-        float mx[kLpUnroll], top;
-#pragma unroll
-        for (int u = 0; u < kLpUnroll; ++u) {
-            mx[u] = vector_max<T>(q[u]);
-            top = u ? fmaxf(top, mx[u]) : mx[u];
-        }
-        if constexpr (TOP) {
-            lane_top = fmaxf(lane_top, top);
-            // a new bound in rounds 0, 1, 2, 4, 8, ...; for long lists in 3, 6, 12, ... too
-            if ((round & (round - 1)) == 0 || (n > 8 && round == 3 * (round & -round))) {
-                publish();
-                if (round == 0) __syncthreads();
-                else __syncwarp();
-                const uint32_t lowest = lowest_vote();
-                all = lowest == 0u;
-                bound = value_of(lowest);
-            }
-            if (__any_sync(0xffffffffu, all || top >= bound)) {
-#pragma unroll
-                for (int u = 0; u < kLpUnroll; ++u) {
-                    const int v = (g_first + g) * kLpChunk + u * 32 + lane;
-                    if (v < row.nvec && mx[u] > -INFINITY && (all || mx[u] >= bound)) {
-                        const int at = atomicAdd(&found, 1);
-                        if (at < kLpAside) aside[at] = q[u], aside_v[at] = v;
-                    }
-                }
-            }
-        }
-        if (top > sums.m) sums.raise(top, c2);
-        add_vectors<T>(q, c2, sums);
-    }
-    if constexpr (TOP) {
-        publish();                                           // read after the next barrier
-        if (round == 0) __syncthreads();                     // a warp without chunks: the others' first round
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -450,10 +482,188 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
         other.t = __shfl_xor_sync(0xffffffffu, sums.t, o);
         sums.merge(other, c2);
     }
-    if (lane == 0) warp_sums[warp] = sums;
-    __syncthreads();
-    sums.init();
-    if (lane < warps) sums = warp_sums[lane];
+    if (CLUSTER) {
+        // every CTA of the cluster gets every warp's sums
+        __syncwarp();
+        cluster_started_wait();
+        if (lane < (int)ctas) {
+            RowSums* p = &warp_sums[rank * warps + warp];
+            st_cluster_f32(&p->m, lane, sums.m);
+            st_cluster_f32(&p->s, lane, sums.s);
+            st_cluster_f32(&p->t, lane, sums.t);
+        }
+        if (TOP) __syncthreads();
+    } else {
+        if (lane == 0) warp_sums[warp] = sums;
+        __syncthreads();
+    }
+    if constexpr (TOP) {
+        // Lists of the first `lists` warps -> one list in warp 0.  Every warp calls it; a warp's
+        // place in list_key is written once per call, before the barrier of its level.
+        auto merge_lists = [&](WarpList& list, int lists) {
+            for (int step = 1; step < lists; step *= 2) {
+                if (warp % (2 * step) == step && warp < lists) {
+                    list_key[warp][lane] = list.key;
+                    list_idx[warp][lane] = list.idx;
+                }
+                __syncthreads();
+                if (warp % (2 * step) == 0 && warp + step < lists)
+                    list.merge_reversed(list_key[warp + step][31 - lane], list_idx[warp + step][31 - lane]);
+            }
+        };
+        // adds an entry per lane to the warp's list, unless none of them beats its n-th
+        auto take = [&](WarpList& list, uint32_t key, uint32_t idx) {
+            const uint32_t last_key = __shfl_sync(0xffffffffu, list.key, a.n_top - 1);
+            const uint32_t last_idx = __shfl_sync(0xffffffffu, list.idx, a.n_top - 1);
+            if (!__any_sync(0xffffffffu, WarpList::beats(key, idx, last_key, last_idx))) return;
+            WarpList next;
+            next.key = key, next.idx = idx;
+            next.sort();
+            list.merge_reversed(__shfl_sync(0xffffffffu, next.key, 31 - lane),
+                                __shfl_sync(0xffffffffu, next.idx, 31 - lane));
+        };
+        // place i of the CTA's list
+        auto put = [&](int i, uint64_t entry) {
+            if (CLUSTER) st_cluster_u64(&lists[rank * n + i], 0, entry);
+            else lists[i] = entry;
+        };
+        bool general = true;
+        if (keep) {
+            // the lanes' shares of chunks that reach the bound; their logits that do; and these ones'
+            // places, by comparing all of them
+            const uint32_t lowest = __reduce_min_sync(0xffffffffu, lane < voters ? vote[lane] : 0xFFFFFFFFu);
+            const uint32_t masked = order_of(-INFINITY);
+            const float last = value_of(lowest);
+            const float last_half = __uint_as_float(__float_as_uint(last) & 0xFFFF0000u);
+            for (int c = warp, k = warp; c < chunks; c += kGroup * warps, k += warps) {
+                const float top = __uint_as_float((uint32_t)kept[k * 32 + lane] << 16);
+                if (top > -INFINITY && (lowest == 0u || top >= last_half)) {
+                    const int at = atomicAdd(&reached, 1);
+                    if (at < kLpRanked) again[at] = (uint32_t)(c * 32 + lane);
+                }
+            }
+            __syncthreads();
+            for (int i = threadIdx.x; i < min(reached, kLpRanked) * (kGroup * kLpUnroll); i += blockDim.x) {
+                const uint32_t share = again[i / (kGroup * kLpUnroll)];
+                const int g = (int)(share / 32) + i / kLpUnroll % kGroup * warps;
+                const int v = (g_first + g) * kLpChunk + i % kLpUnroll * 32 + (int)(share % 32);
+                if (g >= chunks || v >= row.nvec) continue;
+                const int j0 = row.first(v);
+                unsigned hits = 0u;
+                auto test = [&](int e, float x) {
+                    if (x > -INFINITY && (lowest == 0u || x >= last)) hits |= 1u << e;
+                };
+                if (row.whole(v)) {
+                    float x[VEC];
+                    RowView<T>::unpack(ld_v4(row.p + j0), x);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) test(e, x[e]);
+                } else {
+#pragma unroll 1
+                    for (int e = 0; e < VEC; ++e)
+                        if (j0 + e >= 0 && j0 + e < a.V) test(e, to_f32<T>(row.p[j0 + e]));
+                }
+                for (; hits; hits &= hits - 1u) {
+                    const int jj = j0 + __ffs(hits) - 1, at = atomicAdd(&ranked, 1);
+                    if (at < kLpRanked) few[at] = pack_entry(order_of(to_f32<T>(row.p[jj])), (uint32_t)jj);
+                }
+            }
+            __syncthreads();
+            const int j0 = max(0, row.first(g_first * kLpChunk));        // this CTA's first logit
+            const int need = min(n, chunks ? min(a.V, row.first((g_first + chunks) * kLpChunk)) - j0 : 0);
+            // Fewer unmasked logits than places (they have all been set aside then): masked ones
+            // follow, the lowest indices, which are among the first `need`.
+            unsigned rest = 0u;
+            if (ranked < need && lowest <= masked)
+                rest = __ballot_sync(0xffffffffu, lane < need && to_f32<T>(row.p[j0 + lane]) == -INFINITY);
+            if (reached <= kLpRanked && ranked <= kLpRanked && ranked + __popc(rest) >= need) {
+                general = false;
+                // four lanes compare an entry
+                for (int i0 = warp * 8; i0 < ranked; i0 += warps * 8) {
+                    const int i = i0 + lane / 4;
+                    const uint64_t own = i < ranked ? few[i] : ~(uint64_t)0;
+                    int place = 0;
+                    for (int o = lane % 4; o < ranked; o += 4) place += few[o] > own;
+                    place += __shfl_xor_sync(0xffffffffu, place, 1);
+                    place += __shfl_xor_sync(0xffffffffu, place, 2);
+                    if (lane % 4 == 0 && i < ranked && place < n) put(place, own);
+                }
+                if (warp == 0) {
+                    const int place = ranked + __popc(rest & ((1u << lane) - 1u));
+                    if (rest >> lane & 1 && place < need) put(place, pack_entry(masked, (uint32_t)(j0 + lane)));
+                    if (lane >= need && lane < n) put(lane, pack_entry(0u, kNone));
+                }
+            }
+        }
+        if (general) {
+            // The general way, whose work does not depend on the logits: the n best chunks ...
+            uint32_t* chunk_max = reinterpret_cast<uint32_t*>(smem);     // order_of the maximum, at least 1
+            for (int g = warp; g < chunks; g += warps) {
+                uint4 q[kLpUnroll];
+                load_chunk(g, q);
+                const uint32_t o = __reduce_max_sync(0xffffffffu, max(order_of(lane_max<T>(q)), 1u));
+                if (lane == 0) chunk_max[g] = o;
+            }
+            __syncthreads();
+            WarpList list;
+            list.init();
+            for (int g = warp * 32; g < chunks; g += warps * 32)
+                take(list, g + lane < chunks ? chunk_max[g + lane] : 0u, g + lane < chunks ? g + lane : kNone);
+            merge_lists(list, min(warps, (chunks + 31) / 32));
+            if (warp == 0) sel[lane] = list.idx;
+            __syncthreads();
+            // ... the n best vectors of those ...
+            list.init();
+            const int picked = min(n, chunks) * kLpUnroll;
+            for (int i = warp; i < picked; i += warps) {
+                const int v = (g_first + (int)sel[i / kLpUnroll]) * kLpChunk + i % kLpUnroll * 32 + lane;
+                uint32_t key = 0u;
+                if (v < row.nvec) {
+                    float x[VEC];
+                    RowView<T>::unpack(row.load(v, -INFINITY), x);
+                    float mx = x[0];
+    #pragma unroll
+                    for (int e = 1; e < VEC; ++e) mx = fmaxf(mx, x[e]);
+                    key = max(order_of(mx), 1u);
+                }
+                take(list, key, v < row.nvec ? (uint32_t)v : kNone);
+            }
+            __syncthreads();                                     // sel has been read
+            merge_lists(list, min(warps, picked));
+            if (warp == 0) sel[lane] = list.idx;
+            __syncthreads();
+            // ... and the n best logits of those
+            list.init();
+            for (int i = warp * 32 + lane; i - lane < n * VEC; i += warps * 32) {
+                uint32_t key = 0u, idx = kNone;
+                if (i < n * VEC && sel[i / VEC] != kNone) {
+                    const int j = row.first((int)sel[i / VEC]) + i % VEC;
+                    if (j >= 0 && j < a.V) key = order_of(to_f32<T>(row.p[j])), idx = (uint32_t)j;
+                }
+                take(list, key, idx);
+            }
+            merge_lists(list, min(warps, (n * VEC + 31) / 32));
+            if (warp == 0 && lane < n) put(lane, pack_entry(list.key, list.idx));
+        }
+    }
+    // the sums of the row's warps, the same bits in every thread of the cluster
+    if (CLUSTER) {
+        sync_cluster();
+        sums.init();
+        for (int i = lane; i < warps * (int)ctas; i += 32) sums.merge(warp_sums[i], c2);
+#pragma unroll 1
+        for (int o = 16; o >= kLpMaxWarps; o >>= 1) {
+            RowSums other;
+            other.m = __shfl_xor_sync(0xffffffffu, sums.m, o);
+            other.s = __shfl_xor_sync(0xffffffffu, sums.s, o);
+            other.t = __shfl_xor_sync(0xffffffffu, sums.t, o);
+            sums.merge(other, c2);
+        }
+    } else {
+        if (TOP) __syncthreads();
+        sums.init();
+        if (lane < warps) sums = warp_sums[lane];
+    }
     for (int o = kLpMaxWarps / 2; o; o >>= 1) {
         RowSums other;
         other.m = __shfl_xor_sync(0xffffffffu, sums.m, o);
@@ -461,21 +671,9 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
         other.t = __shfl_xor_sync(0xffffffffu, sums.t, o);
         sums.merge(other, c2);
     }
-    // lane 0's, so that every thread holds the same bits
     sums.m = __shfl_sync(0xffffffffu, sums.m, 0);
     sums.s = __shfl_sync(0xffffffffu, sums.s, 0);
     sums.t = __shfl_sync(0xffffffffu, sums.t, 0);
-    if (ctas > 1) {
-        if (threadIdx.x == 0) cta_sums = sums;
-        sync_cluster();
-        sums.init();
-        for (uint32_t k = 0; k < ctas; ++k) {
-            RowSums o;
-            o.m = ld_cluster_f32(&cta_sums.m, k), o.s = ld_cluster_f32(&cta_sums.s, k);
-            o.t = ld_cluster_f32(&cta_sums.t, k);
-            sums.merge(o, c2);
-        }
-    }
     float m = sums.m, ls, entropy;
     if (a.careful || !(fabsf(m) < kFastMax)) {
         // the same in every CTA of the cluster
@@ -503,7 +701,7 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
         __syncthreads();
         cs = warp_careful[0];
         for (int w = 1; w < warps; ++w) cs.merge(warp_careful[w], c2);
-        if (ctas > 1) {
+        if (CLUSTER) {
             if (threadIdx.x == 0) cta_careful = cs;
             sync_cluster();
             cs.init();
@@ -513,6 +711,7 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
                 o.t = ld_cluster_f32(&cta_careful.t, k);
                 cs.merge(o, c2);
             }
+            sync_cluster();                                          // remote sums have been read
         }
         m = cs.m;
         ls = cs.s == 0.f ? -INFINITY : logf(cs.s);                   // 0: masked throughout
@@ -525,12 +724,11 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
     if (entropy < 0.f) entropy = 0.f;                                // by rounding; NaN stays
     const bool empty = ls == -INFINITY;
     auto logp_of = [&](float x) { return empty || x == -INFINITY ? -INFINITY : (x - m) * a.scale - ls; };
-    if (rank == 0 && threadIdx.x == 0) {
+    if (first) {
         if (a.targets) {
-            const Id t = ((const Id*)a.targets)[r];
             float lp = 0.f;
-            if (t >= 0 && (int64_t)t < a.V) lp = logp_of(to_f32<T>(row.p[t]));
-            else if (t >= 0) set_status(a.ws, MOE_ERR_DEVICE_CHECK);
+            if (target >= 0 && (int64_t)target < a.V) lp = logp_of(to_f32<T>(target_logit));
+            else if (target >= 0) set_status(a.ws, MOE_ERR_DEVICE_CHECK);
             a.logp[r] = lp;
         }
         if (a.entropy) a.entropy[r] = entropy;
@@ -539,179 +737,72 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
             a.stats[2 * r + 1] = ls;
         }
     }
-    if constexpr (!TOP) {
-        if (ctas > 1) sync_cluster();                                // remote sums have been read
-        return;
-    }
-
-    // Lists of the first `lists` warps -> one list in warp 0.  Every warp calls it; a warp's
-    // place in list_key is written once per call, before the barrier of its level.
-    auto merge_lists = [&](WarpList& list, int lists) {
-        for (int step = 1; step < lists; step *= 2) {
-            if (warp % (2 * step) == step && warp < lists) {
-                list_key[warp][lane] = list.key;
-                list_idx[warp][lane] = list.idx;
-            }
-            __syncthreads();
-            if (warp % (2 * step) == 0 && warp + step < lists)
-                list.merge_reversed(list_key[warp + step][31 - lane], list_idx[warp + step][31 - lane]);
-        }
-    };
-    // adds an entry per lane to the warp's list, unless none of them beats its n-th
-    auto take = [&](WarpList& list, uint32_t key, uint32_t idx) {
-        const uint32_t last_key = __shfl_sync(0xffffffffu, list.key, a.n_top - 1);
-        const uint32_t last_idx = __shfl_sync(0xffffffffu, list.idx, a.n_top - 1);
-        if (!__any_sync(0xffffffffu, WarpList::beats(key, idx, last_key, last_idx))) return;
-        WarpList next;
-        next.key = key, next.idx = idx;
-        next.sort();
-        list.merge_reversed(__shfl_sync(0xffffffffu, next.key, 31 - lane),
-                            __shfl_sync(0xffffffffu, next.idx, 31 - lane));
-    };
-    auto write_top = [&](int i, uint32_t key, uint32_t idx) {
-        a.top_idx[r * n + i] = (int32_t)idx;
-        a.top_logp[r * n + i] = logp_of(value_of(key));
-    };
-    // place i of the CTA's own list
-    auto put = [&](int i, uint32_t key, uint32_t idx) {
-        if (ctas > 1) cta_list[i] = pack_entry(key, idx);
-        else write_top(i, key, idx);
-    };
-    bool general = true;
-    if (found <= kLpAside) {
-        // of the vectors set aside the logits that reach the last bound, and their places by
-        // comparing all of them
-        const uint32_t lowest = lowest_vote(), masked = order_of(-INFINITY);
-        const float last = value_of(lowest);
-        for (int i = threadIdx.x; i < found * VEC; i += blockDim.x) {
-            const float x = to_f32<T>(reinterpret_cast<const T*>(aside)[i]);
-            const int j = row.first(aside_v[i / VEC]) + i % VEC;
-            if (j < 0 || j >= a.V || !(x > -INFINITY) || !(lowest == 0u || x >= last)) continue;
-            const int at = atomicAdd(&ranked, 1);
-            if (at < kLpRanked) few[at] = pack_entry(order_of(x), (uint32_t)j);
-        }
-        __syncthreads();
-        const int j0 = max(0, row.first(g_first * kLpChunk));        // this CTA's first logit
-        const int need = min(n, chunks ? min(a.V, row.first((g_first + chunks) * kLpChunk)) - j0 : 0);
-        // Fewer unmasked logits than places (they have all been set aside then): masked ones
-        // follow, the lowest indices, which are among the first `need`.
-        unsigned rest = 0u;
-        if (ranked < need && lowest <= masked)
-            rest = __ballot_sync(0xffffffffu, lane < need && to_f32<T>(row.p[j0 + lane]) == -INFINITY);
-        if (ranked <= kLpRanked && ranked + __popc(rest) >= need) {
-            general = false;
-            for (int i = threadIdx.x; i < ranked; i += blockDim.x) {
-                const uint64_t own = few[i];
-                int place = 0;
-                for (int o = 0; o < ranked; ++o) place += few[o] > own;
-                if (place < n) put(place, (uint32_t)(own >> 32), ~(uint32_t)own);
-            }
-            if (warp == 0) {
-                const int place = ranked + __popc(rest & ((1u << lane) - 1u));
-                if (rest >> lane & 1 && place < need) put(place, masked, (uint32_t)(j0 + lane));
-                if (lane >= need && lane < n) put(lane, 0u, kNone);
-            }
-        }
-    }
-    if (general) {
-        // The general way, whose work does not depend on the logits: the n best chunks ...
-        uint32_t* chunk_max = reinterpret_cast<uint32_t*>(smem);     // order_of the maximum, at least 1
-        for (int g = warp; g < chunks; g += warps) {
-            uint4 q[kLpUnroll];
-            load_chunk(g, q);
-            const uint32_t o = __reduce_max_sync(0xffffffffu, max(order_of(lane_max<T>(q)), 1u));
-            if (lane == 0) chunk_max[g] = o;
-        }
-        __syncthreads();
-        WarpList list;
-        list.init();
-        for (int g = warp * 32; g < chunks; g += warps * 32)
-            take(list, g + lane < chunks ? chunk_max[g + lane] : 0u, g + lane < chunks ? g + lane : kNone);
-        merge_lists(list, min(warps, (chunks + 31) / 32));
-        if (warp == 0) sel[lane] = list.idx;
-        __syncthreads();
-        // ... the n best vectors of those ...
-        list.init();
-        const int picked = min(n, chunks) * kLpUnroll;
-        for (int i = warp; i < picked; i += warps) {
-            const int v = (g_first + (int)sel[i / kLpUnroll]) * kLpChunk + i % kLpUnroll * 32 + lane;
-            uint32_t key = 0u;
-            if (v < row.nvec) {
-                float x[VEC];
-                RowView<T>::unpack(row.load(v, -INFINITY), x);
-                float mx = x[0];
+    if constexpr (TOP) {
+        auto write_top = [&](int i, uint64_t entry) {
+            const uint32_t key = (uint32_t)(entry >> 32);
+            a.top_idx[r * n + i] = (int32_t)~(uint32_t)entry;
+            a.top_logp[r * n + i] = logp_of(value_of(key));
+        };
+        if (!CLUSTER) {
+            if (threadIdx.x < n) write_top(threadIdx.x, lists[threadIdx.x]);
+        } else if (rank == 0) {
+            // an entry's place is the number of entries above it in every list, each in order
+            for (int i = threadIdx.x; i < n * (int)ctas; i += blockDim.x) {
+                const uint64_t own = lists[i];
+                int above[kLpMaxCluster] = {}, place = 0;
+#pragma unroll 1
+                for (int step = kMaxTop; step; step /= 2) {
 #pragma unroll
-                for (int e = 1; e < VEC; ++e) mx = fmaxf(mx, x[e]);
-                key = max(order_of(mx), 1u);
-            }
-            take(list, key, v < row.nvec ? (uint32_t)v : kNone);
-        }
-        __syncthreads();                                     // sel has been read
-        merge_lists(list, min(warps, picked));
-        if (warp == 0) sel[lane] = list.idx;
-        __syncthreads();
-        // ... and the n best logits of those
-        list.init();
-        for (int i = warp * 32 + lane; i - lane < n * VEC; i += warps * 32) {
-            uint32_t key = 0u, idx = kNone;
-            if (i < n * VEC && sel[i / VEC] != kNone) {
-                const int j = row.first((int)sel[i / VEC]) + i % VEC;
-                if (j >= 0 && j < a.V) key = order_of(to_f32<T>(row.p[j])), idx = (uint32_t)j;
-            }
-            take(list, key, idx);
-        }
-        merge_lists(list, min(warps, (n * VEC + 31) / 32));
-        if (warp == 0 && lane < n) put(lane, list.key, list.idx);
-    }
-    if (ctas > 1) {
-        // the CTAs' lists, n entries each, by comparing all of them
-        sync_cluster();
-        if (rank == 0) {
-            const int all = n * (int)ctas;                   // <= kLpRanked
-            for (int i = threadIdx.x; i < all; i += blockDim.x)
-                few[i] = ld_cluster_u64(&cta_list[i % n], i / n);
-            __syncthreads();
-            for (int i = threadIdx.x; i < all; i += blockDim.x) {
-                const uint64_t own = few[i];
-                int place = 0;
-                for (int o = 0; o < all; ++o) place += few[o] > own;
-                if (place < n && own != pack_entry(0u, kNone)) write_top(place, (uint32_t)(own >> 32), ~(uint32_t)own);
+                    for (int l = 0; l < kLpMaxCluster; ++l) {
+                        const int at = above[l] + step - 1;
+                        if (l < (int)ctas && at < n && lists[l * n + at] > own) above[l] += step;
+                    }
+                }
+#pragma unroll
+                for (int l = 0; l < kLpMaxCluster; ++l) place += above[l];
+                if (place < n && own != pack_entry(0u, kNone)) write_top(place, own);
             }
         }
-        sync_cluster();                                      // remote lists and sums have been read
     }
 }
 
-template <typename T, bool TOP>
+template <typename T, bool TOP, bool CLUSTER>
 static auto pick_logprobs(int id_bytes) -> void (*)(LogprobArgs) {
-    return id_bytes == 8 ? logprobs_kernel<T, int64_t, TOP> : logprobs_kernel<T, int32_t, TOP>;
+    return id_bytes == 8 ? logprobs_kernel<T, int64_t, TOP, CLUSTER> : logprobs_kernel<T, int32_t, TOP, CLUSTER>;
+}
+template <typename T>
+static auto pick_logprobs(bool top, bool cluster, int id_bytes) -> void (*)(LogprobArgs) {
+    return top ? (cluster ? pick_logprobs<T, true, true>(id_bytes) : pick_logprobs<T, true, false>(id_bytes))
+               : (cluster ? pick_logprobs<T, false, true>(id_bytes) : pick_logprobs<T, false, false>(id_bytes));
 }
 
 cudaError_t launch_token_logprobs(const LogprobCall& c, cudaStream_t stream) {
     if (c.T == 0) return cudaSuccess;
-    LogprobArgs a{c.logits, (int)c.V, c.ld, c.scale, !fast_scale(c.scale), c.targets, c.logp,
+    LogprobArgs a{c.logits, (int)c.V, c.ld, c.scale, !fast_scale(c.scale), 0, c.targets, c.logp,
                   c.entropy, c.stats, c.n_top, c.top_idx, c.top_logp, c.ws};
     const int64_t vec = 16 / (int64_t)dtype_bytes(c.dtype);
     const int64_t chunks = (c.V + 2 * vec - 2) / (vec * kLpChunk) + 1;         // at most, at any alignment
     // Eight warps per row, in a cluster of CTAs while these fill at most 13/16 of the places (not
-    // every place takes a cluster; 128000 FP32, n = 5: 64 rows take 14.4 us in 256 CTAs and 16.4
-    // in 512, 150 rows 25 us in 300 CTAs and 32 in 600).  Many rows: four warps, so that twice
-    // as many rows are in flight and one row's end hides behind more others (8192 x 127901
-    // BF16, n = 8: 345 against 372 us), unless that leaves the last wave of CTAs much emptier
-    // (1300 rows: 80 against 74 us).
-    const int64_t eights = 4 * (int64_t)c.num_sms, fours = 2 * eights;       // CTAs resident at once
-    const int64_t waves8 = (c.T + eights - 1) / eights, waves4 = (c.T + fours - 1) / fours;
-    const int most = c.T > eights && 2 * waves4 * 4 <= waves8 * 5 ? 4 : kLpMaxWarps;
+    // every place takes a cluster; 128000 FP32, n = 5: 76 rows take 14.4 us in 304 CTAs and 16.5
+    // in 608, 150 rows 21 us in 300 CTAs and 25 in 600).  Somewhat more rows than places: four
+    // warps, which all fit at once (128000 FP32, n = 8: 700 rows take 60 us so and 78 in two
+    // waves of eight warps, but 1216 rows 123 and 104).
+    const int64_t eights = 4 * (int64_t)c.num_sms;                             // CTAs resident at once
+    const int most = c.T > eights && c.T <= eights * 5 / 4 ? 4 : kLpMaxWarps;
     int warps = 1, ctas = 1;
     while (warps < most && warps < chunks) warps *= 2;
     while (ctas < kLpMaxCluster && chunks > (int64_t)warps * ctas && c.T * ctas * 2 <= eights * 13 / 16) ctas *= 2;
-    const size_t ahead = c.dtype == MOE_F32 ? 0 : (size_t)warps * kLpChunk * sizeof(uint4);
-    const size_t maxima = c.n_top ? sizeof(uint32_t) * (size_t)((chunks + ctas - 1) / ctas) : 0;
-    const size_t smem = ahead > maxima ? ahead : maxima;
-    void (*k)(LogprobArgs) =
-        c.n_top ? (c.dtype == MOE_F32 ? pick_logprobs<float, true>(c.id_bytes) : pick_logprobs<uint16_t, true>(c.id_bytes))
-                : (c.dtype == MOE_F32 ? pick_logprobs<float, false>(c.id_bytes)
-                                      : pick_logprobs<uint16_t, false>(c.id_bytes));
+    const size_t ahead = (size_t)kLpAhead * warps * kLpChunk * sizeof(uint4);
+    const size_t share = c.n_top ? (size_t)((chunks + ctas - 1) / ctas) : 0;
+    const size_t per = (size_t)(ctas > 1 ? 1 : 2) * warps;
+    const size_t groups = (share + per - 1) / per * warps;           // of chunks c, c + warps, ...
+    a.keep = c.n_top && groups <= kLpKept;
+    const size_t kept = ahead + (a.keep ? 64 * groups : 0), maxima = sizeof(uint32_t) * share;
+    const size_t smem = (c.n_top ? ctas * kMaxTop * sizeof(uint64_t) : 0) + (kept > maxima ? kept : maxima);
+    void (*k)(LogprobArgs) = c.dtype == MOE_F32 ? pick_logprobs<float>(c.n_top > 0, ctas > 1, c.id_bytes)
+                                               : pick_logprobs<uint16_t>(c.n_top > 0, ctas > 1, c.id_bytes);
+    cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kLpMaxSmem);
+    if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg{};
     if (c.T * ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
     cfg.gridDim = dim3((unsigned)(c.T * ctas));

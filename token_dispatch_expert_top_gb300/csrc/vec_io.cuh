@@ -26,12 +26,16 @@ __device__ __forceinline__ uint32_t cluster_nctarank() {
 }
 
 // ------------------------------------------------------------------------ rows
-// Asynchronous 16-byte copy global -> shared (both addresses 16-byte aligned), and the wait
-// for all of this thread's.
+// Asynchronous 16-byte copy global -> shared (both addresses 16-byte aligned); the end of a
+// group of them, and the wait for all of this thread's groups but the last KEEP.
 __device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int KEEP>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(KEEP) : "memory");
+}
 
 // Element types by moe_dtype_t; BF16 travels as its 16 bits.
 template <typename T>
