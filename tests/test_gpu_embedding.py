@@ -128,6 +128,37 @@ def test_embedding_grad_layouts(M, H, pad, shift, gdt, tdt, accumulate):
     _grad_case(M, ids, 50, H, gdt, tdt, scale=-0.7, accumulate=accumulate, pad=pad, shift=shift)
 
 
+# Up to 1024 tokens take one launch, more are sorted first: the same cases on both sides.
+@pytest.mark.parametrize("N", [1000, 1024, 1025, 1500])
+@pytest.mark.parametrize("H,pad,shift", [(1, 0, 0), (9, 0, 0), (264, 8, 0), (520, 3, 1), (2056, 0, 0)])
+@pytest.mark.parametrize("gdt,tdt,accumulate", [(F32, F32, False), (BF16, F32, True), (BF16, BF16, False)])
+def test_embedding_grad_either_way(M, N, H, pad, shift, gdt, tdt, accumulate):
+    rng = np.random.default_rng(N)
+    ids = rng.zipf(1.4, size=N)
+    ids = torch.from_numpy(np.where(ids > 600, -1, ids - 1).astype(np.int32)).cuda()
+    _grad_case(M, ids, 600, H, gdt, tdt, scale=1.7, accumulate=accumulate, pad=pad, shift=shift)
+
+
+@pytest.mark.parametrize("N", [1, 3, 40, 257, 1024, 1100])
+@pytest.mark.parametrize("H", [8, 2048, 4103, 4112])
+def test_embedding_grad_one_id(M, N, H):
+    """One run of every token, whose columns many CTAs share; and two that take turns."""
+    _grad_case(M, torch.full((N,), 2, device="cuda"), 3, H, BF16, F32)
+    _grad_case(M, torch.arange(N, device="cuda") % 2, 3, H, F32, F32, accumulate=True)
+
+
+def test_embedding_grad_orders_of_many_tokens(M):
+    for ids in (list(range(1200)), list(range(1200))[::-1], [7] * 1024 + [8] * 32 + [9], [5] * 33 + [6] * 999 + [5] * 70,
+                [1, 2] * 700, [1199] * 1025, [-1] * 1040):
+        _grad_case(M, torch.tensor(ids, device="cuda"), 1200, 40, F32, F32)
+
+
+def test_embedding_grad_few_tokens_of_a_tall_table(M):
+    """More rows than one CTA marks at a time."""
+    ids = torch.tensor([0, 4095, 4096, 1_299_999, 5, 5, -3], device="cuda")
+    _grad_case(M, ids, 1_300_000, 3, F32, BF16)
+
+
 def test_embedding_grad_orders(M):
     """Sorted, reversed and interleaved tokens; runs that begin and end on range borders."""
     for ids in (list(range(200)), list(range(200))[::-1], [7] * 32 + [8] * 32 + [9], [5] * 33 + [6] * 31 + [5] * 70,
