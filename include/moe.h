@@ -5,6 +5,8 @@
  * (FP32, BF16 or block-scaled MXFP8 on tcgen05 tensor cores), and a gate-weighted
  * combine back to token order; plus one persistent kernel that runs gather,
  * expert FFN and combine as roles on separate SMs.
+ * Around the layer: token embedding, log probabilities and dropout, with their
+ * gradients.
  *
  * The method is the one described on
  *   [MoK-2.37x] "Cursor's MoK achieves 2.37x performance boost on NVIDIA GB300

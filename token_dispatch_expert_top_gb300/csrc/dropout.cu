@@ -48,6 +48,8 @@ __device__ __forceinline__ bool kept(const uint32_t (&w)[4], int i, const Dropou
 // Aligned rows: one thread per group of eight columns (one counter), 16-byte accesses.  Each
 // thread does one group and ends: blocks that write in address order keep the DRAM writes
 // together (zeroing 3.7 GB: 7.8 TB/s so, 6.6 TB/s by a grid that strides over the data).
+// HBM-bound: 16384 x 7168 BF16 with a residual in 104.5 us (6.7 TB/s), 60% of the issue slots
+// taken, most of them by the generator's multiplications.
 constexpr int kDropThreads = 128;
 template <typename T>
 __global__ void __launch_bounds__(kDropThreads) dropout_groups_kernel(const __grid_constant__ DropoutArgs a) {
@@ -79,7 +81,8 @@ __global__ void __launch_bounds__(kDropThreads) dropout_groups_kernel(const __gr
 
 // Any alignment: one warp per 256 columns of a row.  Lane l draws the counter of columns
 // 8l .. 8l+7, but reads and writes every 32nd column, so that the lanes touch neighbouring
-// elements; the decisions travel by shuffles.
+// elements; the decisions travel by shuffles.  4001 x 1409 FP32 in 12.3 us (3.7 TB/s): one
+// short wave after another, the same with blocks of 64 to 512 threads.
 template <typename T>
 __global__ void __launch_bounds__(256) dropout_columns_kernel(const __grid_constant__ DropoutArgs a, int64_t chunks) {
     const int lane = threadIdx.x % 32;

@@ -822,7 +822,7 @@ cudaError_t launch_token_logprobs(const LogprobCall& c, cudaStream_t stream) {
 // d x_j = p_j (g1 + g2 lp_j) + 1[j = t] scale g_logp with g2 = -scale g_entropy and
 // g1 = -scale (g_logp + g_entropy entropy).  dlogits may be the logits' own buffer: a thread
 // reads its elements before it writes them.  The kernel moves each logit in and its
-// gradient out once, HBM-bound: 4096 x 128000 BF16 in 294 us (7.1 TB/s, part of the logits still in
+// gradient out once, HBM-bound: 4096 x 128000 BF16 in 295 us (7.1 TB/s, part of the logits still in
 // L2).  That leaves about 20 instructions per BF16 logit: whole blocks of a row away from its
 // ends and its target take a path without checks (with them it issued 21 and took 365 us).
 struct LogprobGradArgs {
