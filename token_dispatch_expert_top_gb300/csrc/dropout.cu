@@ -48,11 +48,12 @@ __device__ __forceinline__ bool kept(const uint32_t (&w)[4], int i, const Dropou
 // Aligned rows: one thread per group of eight columns (one counter), 16-byte accesses.  Each
 // thread does one group and ends: blocks that write in address order keep the DRAM writes
 // together (zeroing 3.7 GB: 7.8 TB/s so, 6.6 TB/s by a grid that strides over the data).
-// HBM-bound: 16384 x 7168 BF16 with a residual in 104.5 us (6.7 TB/s), 60% of the issue slots
+// HBM-bound: 16384 x 7168 BF16 with a residual in 102 us (6.9 TB/s), 60% of the issue slots
 // taken, most of them by the generator's multiplications.
 constexpr int kDropThreads = 128;
 template <typename T>
 __global__ void __launch_bounds__(kDropThreads) dropout_groups_kernel(const __grid_constant__ DropoutArgs a) {
+    grid_dependency_wait();
     const uint64_t b = (uint64_t)blockIdx.x * kDropThreads + threadIdx.x;
     uint64_t r = 0;
     if (a.rows == 1) {
@@ -81,10 +82,11 @@ __global__ void __launch_bounds__(kDropThreads) dropout_groups_kernel(const __gr
 
 // Any alignment: one warp per 256 columns of a row.  Lane l draws the counter of columns
 // 8l .. 8l+7, but reads and writes every 32nd column, so that the lanes touch neighbouring
-// elements; the decisions travel by shuffles.  4001 x 1409 FP32 in 12.3 us (3.7 TB/s): one
+// elements; the decisions travel by shuffles.  4001 x 1409 FP32 in 10.3 us (4.4 TB/s): one
 // short wave after another, the same with blocks of 64 to 512 threads.
 template <typename T>
 __global__ void __launch_bounds__(256) dropout_columns_kernel(const __grid_constant__ DropoutArgs a, int64_t chunks) {
+    grid_dependency_wait();
     const int lane = threadIdx.x % 32;
     const int64_t item = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
     const int64_t r = item / chunks;
@@ -137,19 +139,12 @@ cudaError_t launch_dropout(const void* x, int dtype, int64_t rows, int64_t cols,
         a.key[i][1] = (uint32_t)(seed >> 32) + i * 0xBB67AE85u;
     }
     if (rows > (1ll << 60) / a.groups) return cudaErrorInvalidValue;
-    if (vec) {
-        const int64_t grid = (rows * a.groups + kDropThreads - 1) / kDropThreads;
-        if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-        if (dtype == MOE_F32) dropout_groups_kernel<float><<<(unsigned)grid, kDropThreads, 0, stream>>>(a);
-        else dropout_groups_kernel<uint16_t><<<(unsigned)grid, kDropThreads, 0, stream>>>(a);
-    } else {
-        const int64_t chunks = (cols + 255) / 256;
-        const int64_t grid = (rows * chunks + 7) / 8;
-        if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-        if (dtype == MOE_F32) dropout_columns_kernel<float><<<(unsigned)grid, 256, 0, stream>>>(a, chunks);
-        else dropout_columns_kernel<uint16_t><<<(unsigned)grid, 256, 0, stream>>>(a, chunks);
-    }
-    return cudaGetLastError();
+    if (vec)
+        return launch_after(dtype == MOE_F32 ? dropout_groups_kernel<float> : dropout_groups_kernel<uint16_t>,
+                            (rows * a.groups + kDropThreads - 1) / kDropThreads, kDropThreads, 0, 1, stream, a);
+    const int64_t chunks = (cols + 255) / 256;
+    return launch_after(dtype == MOE_F32 ? dropout_columns_kernel<float> : dropout_columns_kernel<uint16_t>,
+                        (rows * chunks + 7) / 8, 256, 0, 1, stream, a, chunks);
 }
 
 }  // namespace moe

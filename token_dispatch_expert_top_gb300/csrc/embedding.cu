@@ -86,14 +86,15 @@ struct RawCols {
 
 // A memory-bound copy with a scale.  Short rows (aligned, at most 128 columns): 2^lane_bits
 // lanes per row, each one group of eight columns.  Otherwise one warp per 256 * U columns of
-// a row; its loads are all issued before the first store.  8192 rows of 7168 BF16 in 32.8 us
-// (7.1 TB/s); a single row is bound by the launch.
+// a row; its loads are all issued before the first store.  8192 rows of 7168 BF16 in 30.1 us
+// (7.7 TB/s, some of it L2's); a single row is bound by the launch.
 constexpr int kEmbedUnroll = 4;
 template <typename Id, typename In, typename Out, bool VECTOR>
 __global__ void __launch_bounds__(256) embedding_kernel(const Id* __restrict__ ids, int64_t N,
                                                         const In* __restrict__ table, int64_t V, int64_t H,
                                                         int64_t ld_table, float scale, Out* __restrict__ out,
                                                         int64_t ld_out, int chunks, int lane_bits, WsHeader* ws) {
+    grid_dependency_wait();
     const int lane = threadIdx.x % 32;
     const uint64_t item = (uint64_t)blockIdx.x * 8 + threadIdx.x / 32;
     if (lane_bits < 5) {
@@ -141,11 +142,9 @@ static cudaError_t launch_embedding_t(const void* ids, int64_t N, const void* ta
     const int64_t chunks = lane_bits < 5 ? 1 : (H + 256 * kEmbedUnroll - 1) / (256 * kEmbedUnroll);
     const int64_t items = lane_bits < 5 ? (N + (32 >> lane_bits) - 1) >> (5 - lane_bits) : N * chunks;
     const int64_t grid = (items + 7) / 8;
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     auto* k = vec ? embedding_kernel<Id, In, Out, true> : embedding_kernel<Id, In, Out, false>;
-    k<<<(unsigned)grid, 256, 0, stream>>>((const Id*)ids, N, (const In*)table, V, H, ld_table, scale, (Out*)out,
-                                          ld_out, (int)chunks, lane_bits, ws);
-    return cudaGetLastError();
+    return launch_after(k, grid, 256, 0, 1, stream, (const Id*)ids, N, (const In*)table, V, H, ld_table, scale,
+                        (Out*)out, ld_out, (int)chunks, lane_bits, ws);
 }
 
 template <typename Id>
@@ -300,6 +299,7 @@ __global__ void __launch_bounds__(kOrderThreads)
                        int32_t* __restrict__ key, int32_t* __restrict__ n_live, uint32_t* __restrict__ present,
                        int fill_from, Grad* __restrict__ dtable, int64_t H, int64_t ld, WsHeader* ws) {
     grid_dependents_launch();
+    grid_dependency_wait();
     if ((int)blockIdx.x >= fill_from) {
         const int64_t warps = (int64_t)(gridDim.x - fill_from) * (kOrderThreads / 32);
         for (int64_t v = (int64_t)(blockIdx.x - fill_from) * (kOrderThreads / 32) + threadIdx.x / 32; v < V; v += warps)
@@ -459,29 +459,12 @@ __global__ void __launch_bounds__(kFillThreads)
     }
 }
 
-// Launches a kernel that waits on the device for the one before it in the stream, so that its
-// launch overlaps that one's end.
-template <typename... Params, typename... Args>
-static cudaError_t launch_after(void (*k)(Params...), int64_t blocks, int threads, cudaStream_t stream,
-                                const Args&... args) {
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.stream = stream;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k, args...);
-}
-
 template <typename Grad>
 static cudaError_t launch_fill_t(const EmbedBackward& c, cudaStream_t stream) {
     const int64_t row_bytes = c.H * (int64_t)sizeof(Grad);
     const int fill_rows = row_bytes > kFillBytes / 2 ? 1 : (int)(kFillBytes / row_bytes);
     const int64_t blocks = (c.V + fill_rows - 1) / fill_rows;
-    return launch_after(embed_fill_kernel<Grad>, blocks, kFillThreads, stream, (const uint32_t*)c.present, c.V, c.H,
+    return launch_after(embed_fill_kernel<Grad>, blocks, kFillThreads, 0, 1, stream, (const uint32_t*)c.present, c.V, c.H,
                         (Grad*)c.dtable, c.ld_dtable, fill_rows);
 }
 
@@ -634,8 +617,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinCtas) embed_join_kernel(
 // as it has tokens, and nothing is exchanged between CTAs.  In a CTA, 2^bits neighbouring lanes
 // hold a row's groups and the others the run's next rows; their FP32 sums are added in
 // pairs.  The first `zero_ctas` CTAs set the rows that no token names to zero, `zero_rows` each.
-//   777 rows of 1409 FP32 columns into 5003: 11.0 us against 17.2 by sorting (12.9 with three or
-// five CTAs to an SM); one id for all of 1000 rows of 2048: 9.7 against 19.7.  Every CTA reads all
+//   777 rows of 1409 FP32 columns into 5003: 9.8 us; with nothing else in the stream to overlap
+// 11.0 against 17.2 by sorting (12.9 with three or five CTAs to an SM); one id for all of 1000 rows of 2048: 9.7 against 19.7.  Every CTA reads all
 // ids, so the work grows with N^2: at 2000 tokens it took 27.2 us against 18.8.
 constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32;
 constexpr int kFewTokens = 1024, kFewSweeps = kFewTokens / kFewThreads;
@@ -663,6 +646,7 @@ __global__ void __launch_bounds__(kFewThreads, 4) embed_few_kernel(const __grid_
     __shared__ uint32_t words[kFewZeroRows / 32];
     __shared__ uint16_t list[kFewTokens];
     __shared__ float sums[8][kFewThreads];
+    grid_dependency_wait();
     const Id* ids = (const Id*)a.ids;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     bool bad = false;
@@ -822,8 +806,7 @@ static cudaError_t launch_few_t(const EmbedBackward& c, cudaStream_t stream) {
     const int64_t blocks = a.zero_ctas + c.N * a.slices;
     if (blocks == 0) return cudaSuccess;
     auto* k = vec ? embed_few_kernel<Id, In, Grad, true> : embed_few_kernel<Id, In, Grad, false>;
-    k<<<(unsigned)blocks, kFewThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_after(k, blocks, kFewThreads, 0, 1, stream, a);
 }
 template <typename Id>
 static cudaError_t launch_few_id(const EmbedBackward& c, cudaStream_t stream) {
@@ -845,10 +828,9 @@ static cudaError_t launch_order_t(const EmbedBackward& c, bool fill, cudaStream_
                                            (int)order_smem(kOrderRange));
     if (err != cudaSuccess) return err;
     const int64_t fill_ctas = !fill ? 0 : (c.V + 31) / 32 < 2 * c.num_sms ? (c.V + 31) / 32 : 2 * c.num_sms;
-    embed_order_kernel<Id, Grad><<<(unsigned)(grid + fill_ctas), kOrderThreads, order_smem((int)range), stream>>>(
-        (const Id*)c.ids, (int)c.N, c.V, (int)range, c.order, c.key, c.n_live, c.present, (int)grid, (Grad*)c.dtable,
-        c.H, c.ld_dtable, c.ws);
-    return cudaGetLastError();
+    return launch_after(embed_order_kernel<Id, Grad>, grid + fill_ctas, kOrderThreads, order_smem((int)range), 1,
+                        stream, (const Id*)c.ids, (int)c.N, c.V, (int)range, c.order, c.key, c.n_live, c.present,
+                        (int)grid, (Grad*)c.dtable, c.H, c.ld_dtable, c.ws);
 }
 
 template <typename In, typename Grad>
@@ -875,11 +857,11 @@ static cudaError_t launch_sums_t(const EmbedBackward& c, cudaStream_t stream) {
     if ((int64_t)a.ranges * a.chunks > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (blocks == 0) return cudaSuccess;
     auto* k = vec ? embed_segment_kernel<In, Grad, true> : embed_segment_kernel<In, Grad, false>;
-    cudaError_t err = launch_after(k, blocks, kSumWarps * 32, stream, a);
+    cudaError_t err = launch_after(k, blocks, kSumWarps * 32, 0, 1, stream, a);
     if (err != cudaSuccess || a.ranges <= 1) return err;          // one range: no run crosses
     auto* j = vec ? embed_join_kernel<Grad, true> : embed_join_kernel<Grad, false>;
     const int64_t most = (int64_t)(a.ranges - 1) * ((a.chunks + kJoinCols - 1) / kJoinCols);   // items
-    return launch_after(j, most < kJoinCtas * c.num_sms ? most : kJoinCtas * c.num_sms, kJoinWarps * 32, stream, a);
+    return launch_after(j, most < kJoinCtas * c.num_sms ? most : kJoinCtas * c.num_sms, kJoinWarps * 32, 0, 1, stream, a);
 }
 
 // Tables and token rows (written twice then) of at most so many bytes are zeroed beside the

