@@ -90,9 +90,8 @@ struct RawCols {
 // (7.7 TB/s, some of it L2's); a single row is bound by the launch.
 constexpr int kEmbedUnroll = 4;
 template <typename Id, typename In, typename Out, bool VECTOR>
-__global__ void __launch_bounds__(256) embedding_kernel(const Id* __restrict__ ids, int64_t N,
-                                                        const In* __restrict__ table, int64_t V, int64_t H,
-                                                        int64_t ld_table, float scale, Out* __restrict__ out,
+__global__ void __launch_bounds__(256) embedding_kernel(const Id* ids, int64_t N, const In* table, int64_t V,
+                                                        int64_t H, int64_t ld_table, float scale, Out* out,
                                                         int64_t ld_out, int chunks, int lane_bits, WsHeader* ws) {
     grid_dependency_wait();
     const int lane = threadIdx.x % 32;
@@ -295,9 +294,8 @@ __device__ __forceinline__ void zero_row(Grad* row, int64_t H, int t, int thread
 // launch of embed_fill_kernel; the rows that tokens name are written over by the sums.
 template <typename Id, typename Grad>
 __global__ void __launch_bounds__(kOrderThreads)
-    embed_order_kernel(const Id* __restrict__ ids, int N, int64_t V, int range, int32_t* __restrict__ order,
-                       int32_t* __restrict__ key, int32_t* __restrict__ n_live, uint32_t* __restrict__ present,
-                       int fill_from, Grad* __restrict__ dtable, int64_t H, int64_t ld, WsHeader* ws) {
+    embed_order_kernel(const Id* ids, int N, int64_t V, int range, int32_t* order, int32_t* key, int32_t* n_live,
+                       uint32_t* present, int fill_from, Grad* dtable, int64_t H, int64_t ld, WsHeader* ws) {
     grid_dependents_launch();
     grid_dependency_wait();
     if ((int)blockIdx.x >= fill_from) {
@@ -444,8 +442,7 @@ constexpr int kFillBytes = 16384;             // about what one CTA fills
 // the look at `present`.
 template <typename Grad>
 __global__ void __launch_bounds__(kFillThreads)
-    embed_fill_kernel(const uint32_t* __restrict__ present, int64_t V, int64_t H, Grad* __restrict__ dtable,
-                      int64_t ld, int fill_rows) {
+    embed_fill_kernel(const uint32_t* present, int64_t V, int64_t H, Grad* dtable, int64_t ld, int fill_rows) {
     grid_dependency_wait();
     if (fill_rows == 1) {
         const uint32_t v = blockIdx.x;

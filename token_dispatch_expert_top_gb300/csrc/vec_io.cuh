@@ -11,6 +11,9 @@ namespace moe {
 // ------------------------------------------------- launches that overlap their predecessor
 // Waits until the kernel before this one in the stream has finished and its writes are
 // visible (for kernels launched with programmatic stream serialization; otherwise at once).
+// Such a kernel's inputs may still be written while its blocks are resident, so none of them is
+// declared `const __restrict__`: that would promise that they are constant for the kernel's whole
+// life, and allow loads that are not coherent or that begin before this wait.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Lets such a kernel's blocks start, up to their wait, as soon as every block of this one has
 // come here.
