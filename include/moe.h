@@ -536,7 +536,8 @@ int moe_embedding(const void* ids, int id_bytes, int64_t N, const void* table, i
  * with it only the rows that tokens name are touched.  Negative ids take no part; an id
  * of V or more takes none and records MOE_ERR_DEVICE_CHECK.
  *   dout : [N][H] (dout_dtype);  dtable : [V][H] (dtable_dtype)             (out)
- *   workspace : moe_embedding_workspace_bytes(N, V, H) bytes (0 for an invalid shape) */
+ *   workspace : moe_embedding_workspace_bytes(N, V, H) bytes (0 for an invalid shape),
+ *               which grows with N: one for N tokens serves every smaller batch, too */
 size_t moe_embedding_workspace_bytes(int64_t N, int64_t V, int64_t H);
 int moe_embedding_backward(const void* ids, int id_bytes, int64_t N, int64_t V, int64_t H,
                            const void* dout, int dout_dtype, int64_t ld_dout, float scale,

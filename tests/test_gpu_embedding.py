@@ -211,3 +211,18 @@ def test_embedding_on_another_stream(M):
     assert torch.equal(out, table[ids])
     ref = torch.zeros(V, H, dtype=torch.float64, device="cuda").index_add_(0, ids, dout.double())
     assert float((dtable.double() - ref).abs().max()) < 64 * 2.0 ** -24 * 64
+
+
+@pytest.mark.parametrize("longest,N,H", [(8192, 8160, 2048), (1170, 1162, 3584), (2400, 1100, 1409)])
+def test_embedding_grad_in_a_longer_batchs_workspace(M, longest, N, H):
+    """One workspace for the longest batch serves a shorter one, whose ranges are shorter."""
+    V = 700
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    ids = torch.randint(-1, V, (N,), device="cuda", generator=gen)
+    dout = torch.randint(-8, 9, (N, H), device="cuda", generator=gen).float()
+    ws = _ws(M, M.moe_embedding_workspace_bytes(longest, V, H))
+    dtable = torch.full((V, H), 5.0, device="cuda")
+    M.moe_embedding_backward(ids, dout, dtable, 1.0, False, ws)
+    ref = torch.zeros((V, H), device="cuda").index_add_(0, ids.clamp(min=0), dout * (ids >= 0).unsqueeze(1))
+    assert torch.equal(dtable, ref)                        # whole numbers: exact in any order
+    assert M.moe_last_device_status(ws) == M.MOE_OK

@@ -48,6 +48,15 @@ def test_embedding_workspace_bytes():
     assert f(1 << 16, 1000, 7168) >= (1 << 16) * 8
 
 
+@pytest.mark.parametrize("H", [1, 64, 256, 257, 1409, 2048, 7168, 100_000])
+def test_a_longer_batchs_embedding_workspace_serves_a_shorter_one(H):
+    f = M.moe_embedding_workspace_bytes
+    sizes = [f(n, 32000, H) for n in range(0, 20_000)]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+    wide = [f(n, 32000, H) for n in range(20_000, 1 << 30, 7_654_321)]
+    assert sizes[-1] <= wide[0] and all(a <= b for a, b in zip(wide, wide[1:]))
+
+
 def _logp(logits=16, dt=1, T=4, V=64, ld=64, scale=1.0, targets=16, id_bytes=4, logp=16, entropy=16, stats=16,
           n_top=2, ti=16, tl=16, ws=None, wsb=0):
     return M.lib().moe_token_logprobs(logits, dt, T, V, ld, scale, targets, id_bytes, logp, entropy, stats, n_top,

@@ -295,11 +295,12 @@ EmbedPlan make_embed_plan(int64_t N, int64_t V, int64_t H) {
         return o;
     };
     pl.n_live = take(3 * sizeof(int32_t));
-    pl.crossing = take(sizeof(int4) * (size_t)embed_ranges(N, H));
+    const size_t ranges = (size_t)embed_ranges_room(N, H);
+    pl.crossing = take(sizeof(int4) * ranges);
     pl.order = take(sizeof(int32_t) * (size_t)N);
     pl.key = take(sizeof(int32_t) * (size_t)N);
     pl.present = take(sizeof(uint32_t) * (size_t)((V + 31) / 32));
-    pl.part = take(sizeof(float) * 2 * (size_t)embed_ranges(N, H) * (size_t)((H + 255) / 256 * 256));
+    pl.part = take(sizeof(float) * 2 * ranges * (size_t)((H + 255) / 256 * 256));
     pl.total = off;
     return pl;
 }

@@ -220,6 +220,14 @@ inline int embed_ranges(int64_t N, int64_t H) {
     const int places = embed_places(N, H);
     return (int)((N + places - 1) / places);
 }
+// At least embed_ranges of any batch of N tokens or fewer, and growing with N: a workspace for N
+// serves those, too.  Ranges of 2 p < 32 tokens are only cut from batches that they split into fewer
+// than 2048 / chunks ranges, so ranges of p number at most twice that.
+inline int64_t embed_ranges_room(int64_t N, int64_t H) {
+    const int64_t chunks = (H + 255) / 256, short_ranges = (N + 3) / 4, most = 2 * ((2048 + chunks - 1) / chunks);
+    const int64_t long_ranges = (N + 31) / 32, bounded = short_ranges < most ? short_ranges : most;
+    return long_ranges > bounded ? long_ranges : bounded;
+}
 struct EmbedBackward {
     const void* ids;
     int id_bytes;
