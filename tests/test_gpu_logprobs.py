@@ -310,3 +310,29 @@ def test_same_bits_every_time(M):
     x, t = _logits(64, 40001, BF16, seed=12), _targets(64, 40001)
     a, b = _forward(M, x, t, 1.0, 8), _forward(M, x, t, 1.0, 8)
     assert all(torch.equal(a[k], b[k]) for k in a)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,V", [(4, 3000), (700, 3000), (4, 50001)])
+@pytest.mark.parametrize("bad", [float("nan"), INF])
+def test_a_row_with_nan_or_infinity_gives_nan_for_masked_tokens_too(M, T, V, dtype, bad):
+    """The sum of such a row is no number, so neither is any log probability read off it:
+    those of a masked target and of the masked ends of the top list among them."""
+    x = _logits(T, V, dtype, seed=4)
+    t = _targets(T, V).int()
+    x[1] = -INF
+    x[1, [7, 1000, 2900]] = torch.tensor([0.5, bad, 1.0], device="cuda", dtype=dtype)
+    t[1] = 11                                              # masked
+    x[2] = -INF
+    x[2, 2000] = bad                                       # nothing else left
+    t[2] = 2999
+    x[3, ::2] = -INF
+    x[3, 5] = bad
+    t[3] = 4
+    o = _forward(M, x, t, 0.7, 8)
+    for r in (1, 2, 3):
+        assert torch.isnan(o["logp"][r]) and torch.isnan(o["entropy"][r])
+        assert torch.isnan(o["top_logp"][r]).all()
+        idx = o["top_idx"][r]
+        assert int(idx.min()) >= 0 and int(idx.max()) < V and len(set(idx.tolist())) == 8
+    assert bool(torch.isfinite(o["logp"][0])) and bool(torch.isfinite(o["top_logp"][0]).all())

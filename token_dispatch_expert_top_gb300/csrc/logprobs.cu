@@ -724,7 +724,8 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
     }
     if (entropy < 0.f) entropy = 0.f;                                // by rounding; NaN stays
     const bool empty = ls == -INFINITY;
-    auto logp_of = [&](float x) { return empty || x == -INFINITY ? -INFINITY : (x - m) * a.scale - ls; };
+    // (-inf for a masked logit, but NaN where the row's sum is)
+    auto logp_of = [&](float x) { return empty ? -INFINITY : (x - m) * a.scale - ls; };
     if (first) {
         if (a.targets) {
             float lp = 0.f;
