@@ -336,3 +336,67 @@ def test_a_row_with_nan_or_infinity_gives_nan_for_masked_tokens_too(M, T, V, dty
         idx = o["top_idx"][r]
         assert int(idx.min()) >= 0 and int(idx.max()) < V and len(set(idx.tolist())) == 8
     assert bool(torch.isfinite(o["logp"][0])) and bool(torch.isfinite(o["top_logp"][0]).all())
+
+
+def _far_logits(T, V, scale):
+    """Normal FP32 logits that `scale` brings to about 0 .. 13 below a row's largest."""
+    gen = torch.Generator(device="cuda").manual_seed(T + V)
+    z = torch.rand((T, V), generator=gen, device="cuda", dtype=torch.float64)
+    if scale > 1:
+        return (2.0 ** -126 * (1 + 4 * z)).float()         # 3e38 of these: 3.5 .. 17.6
+    x = ((2 * z - 1) * 3.4e38).float()                     # 1e-38 of these: -3.4 .. 3.4
+    x[0, :V // 2] = torch.finfo(F32).max                   # differences that pass FP32's range
+    x[0, V // 2:] = -torch.finfo(F32).max
+    return x
+
+
+@pytest.mark.parametrize("scale", [3e38, 2.0 ** 127, 1e-38, 2.0 ** -126])
+@pytest.mark.parametrize("T,V", [(3, 600), (3, 50001), (700, 2500)])
+def test_scales_at_the_ends_of_fp32(M, T, V, scale):
+    """Every positive finite scale is accepted: with the largest, scale log2 e passes FP32's range,
+    with the smallest the logits' differences and their sums do."""
+    x, t = _far_logits(T, V, scale), _targets(T, V, low=-1)
+    _check(M, x, t, scale, 5, grad=T < 10)
+
+
+@pytest.mark.parametrize("scale", [3e38, 1e-38, 2.0 ** -126])
+def test_gradients_at_scales_at_the_ends_of_fp32(M, scale):
+    """With gradients that bring the results back into FP32's range."""
+    T, V = 6, 901
+    x, t = _far_logits(T, V, scale), _targets(T, V)
+    x[1] = x[1].min()
+    x[1, t[1]] = x[1].abs().max() * 200 if scale > 1 else x[2].max()
+    s, back = float(np.float32(scale)), 1e-30 if scale > 1 else 1e30
+    o = _forward(M, x, t, scale, 0)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    gl, gh = (torch.randn(T, device="cuda", generator=g) * back for _ in range(2))
+    d = torch.full((T, V), 9.0, device="cuda")
+    M.moe_token_logprobs_backward(x, t, o["stats"], o["entropy"], gl, gh, d, scale)
+    xf, tf = to_np(x).astype(np.float64), to_np(t)
+    al, ah = to_np(gl).astype(np.float64), to_np(gh).astype(np.float64)
+    _, ent, lp = P.token_logprobs(xf, tf, s)
+    ref, p, eps = P.token_logprobs_grad(xf, tf, s, al, ah), np.exp(lp), _eps(V)
+    dist = np.abs(s * (xf - xf.max(1, keepdims=True)))
+    lp_tol = dist * 2.0 ** -22 + eps + np.abs(lp) * 2.0 ** -23
+    bracket = np.abs(al)[:, None] + np.abs(ah)[:, None] * (np.abs(lp) + ent[:, None] + 1)
+    p_rel = eps + (np.abs(lp) + dist + 4) * 2.0 ** -22
+    tol = s * (p * bracket * (2 * p_rel + 2.0 ** -21) + np.abs(ah)[:, None] * p * (lp_tol + (4 + 2 * ent)[:, None] * eps)
+               + np.abs(al)[:, None] * 2.0 ** -22 * (p > 0)) + 2.0 ** -23 * np.abs(ref)
+    _close(to_np(d), ref, tol + 1e-37 * back)
+
+
+def test_a_certain_token_at_the_largest_scale_has_no_gradient(M):
+    """One token that is certain: g_logp (1 - p) is 0, although scale g_logp is past FP32's range."""
+    V, scale = 900, 3e38
+    x = torch.full((2, V), -4.0, device="cuda")
+    x[:, 100] = 4.0
+    t = torch.tensor([100, 5], device="cuda")
+    o = _forward(M, x, t, scale, 1)
+    assert o["logp"].tolist() == [0.0, -INF] and not o["entropy"].any()
+    g = torch.full((2,), 10.0, device="cuda")
+    d = torch.full((2, V), 9.0, device="cuda")
+    M.moe_token_logprobs_backward(x, t, o["stats"], o["entropy"], g, g, d, scale)
+    assert not d[0].any()
+    want = torch.zeros(V, device="cuda")
+    want[5], want[100] = INF, -INF
+    assert torch.equal(d[1], want)

@@ -78,29 +78,37 @@ struct RowSums {
     }
 };
 
-// The same for any row and scale: s = sum exp(c d), t = sum d exp(c d),
-// d = x - m.  m starts at the lowest finite value, so masked logits give d = -inf, exp 0.
+// c (x - m), 0 or below, for any two logits and scale: the difference may pass FP32's range where c
+// brings it back (their halves' does not).
+__device__ __forceinline__ float scaled_difference(float x, float m, float scale) {
+    const float d = x - m;
+    return d == -INFINITY && x != -INFINITY ? 2.f * ((0.5f * x - 0.5f * m) * scale) : d * scale;
+}
+
+// The same for any row and scale: s = sum e^z, t = sum z e^z, z = c (x - m).  (The scale comes
+// before log2 e: the two's product may pass FP32's range.)  m starts at the lowest finite value, so
+// masked logits give z = -inf, e^z = 0.
 struct CarefulSums {
     float m, s, t;
     __device__ void init() {
         m = -FLT_MAX;
         s = t = 0.f;
     }
-    __device__ void raise(float m2, float c2) {
-        const float d = m - m2, f = exp2_approx(d * c2);
-        t = f > 0.f ? f * fmaf(d, s, t) : 0.f;       // f = 0 may meet d = -inf
+    __device__ void raise(float m2, float scale) {
+        const float z = scaled_difference(m, m2, scale), f = exp2_approx(z * kLog2e);
+        t = f > 0.f ? f * fmaf(z, s, t) : 0.f;       // f = 0 may meet z = -inf
         s *= f;
         m = m2;
     }
-    __device__ void add(float x, float c2) {
-        if (x > m) raise(x, c2);
-        const float d = x - m, e = exp2_approx(d * c2);
+    __device__ void add(float x, float scale) {
+        if (x > m) raise(x, scale);
+        const float z = scaled_difference(x, m, scale), e = exp2_approx(z * kLog2e);
         s += e;
-        t = fmaf(e, fmaxf(d, -FLT_MAX), t);          // a masked logit's 0 * -inf is 0
+        t = fmaf(e, fmaxf(z, -FLT_MAX), t);          // a masked logit's 0 * -inf is 0
     }
-    __device__ void merge(CarefulSums o, float c2) {
-        if (o.m > m) raise(o.m, c2);
-        else o.raise(m, c2);
+    __device__ void merge(CarefulSums o, float scale) {
+        if (o.m > m) raise(o.m, scale);
+        else o.raise(m, scale);
         s += o.s;
         t += o.t;
     }
@@ -688,7 +696,7 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
                 float x[VEC];
                 RowView<T>::unpack(q[u], x);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) cs.add(x[i], c2);
+                for (int i = 0; i < VEC; ++i) cs.add(x[i], a.scale);
             }
         }
         for (int o = 16; o; o >>= 1) {
@@ -696,12 +704,12 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
             other.m = __shfl_xor_sync(0xffffffffu, cs.m, o);
             other.s = __shfl_xor_sync(0xffffffffu, cs.s, o);
             other.t = __shfl_xor_sync(0xffffffffu, cs.t, o);
-            cs.merge(other, c2);
+            cs.merge(other, a.scale);
         }
         if (lane == 0) warp_careful[warp] = cs;
         __syncthreads();
         cs = warp_careful[0];
-        for (int w = 1; w < warps; ++w) cs.merge(warp_careful[w], c2);
+        for (int w = 1; w < warps; ++w) cs.merge(warp_careful[w], a.scale);
         if (CLUSTER) {
             if (threadIdx.x == 0) cta_careful = cs;
             sync_cluster();
@@ -710,13 +718,13 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
                 CarefulSums o;
                 o.m = ld_cluster_f32(&cta_careful.m, k), o.s = ld_cluster_f32(&cta_careful.s, k);
                 o.t = ld_cluster_f32(&cta_careful.t, k);
-                cs.merge(o, c2);
+                cs.merge(o, a.scale);
             }
             sync_cluster();                                          // remote sums have been read
         }
         m = cs.m;
         ls = cs.s == 0.f ? -INFINITY : logf(cs.s);                   // 0: masked throughout
-        entropy = cs.s == 0.f ? 0.f : ls - a.scale * (cs.t / cs.s);
+        entropy = cs.s == 0.f ? 0.f : ls - cs.t / cs.s;
     } else {
         const float l2 = log2f(sums.s);
         ls = kLn2 * l2;
@@ -725,7 +733,7 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
     if (entropy < 0.f) entropy = 0.f;                                // by rounding; NaN stays
     const bool empty = ls == -INFINITY;
     // (-inf for a masked logit, but NaN where the row's sum is)
-    auto logp_of = [&](float x) { return empty ? -INFINITY : (x - m) * a.scale - ls; };
+    auto logp_of = [&](float x) { return empty ? -INFINITY : scaled_difference(x, m, a.scale) - ls; };
     if (first) {
         if (a.targets) {
             float lp = 0.f;
@@ -846,7 +854,7 @@ __device__ __forceinline__ F2 grad_pair(F2 x, const GradRow& g) {
 }
 // The same for any logit: a masked one, whose 0 * -inf is 0 here, and any row.
 __device__ __forceinline__ float grad_one(float x, const GradRow& g) {
-    float lp = (x - g.m) * g.scale - g.ls;
+    float lp = scaled_difference(x, g.m, g.scale) - g.ls;
     if (lp < -1e4f) lp = -1e4f;                                      // NaN stays
     const float e = exp2_approx(lp * (0.5f * kLog2e));
     return e * e * fmaf(lp, g.g2, g.g1);
@@ -877,14 +885,16 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const __gri
     g.scale = a.scale;
     int t = -1;
     float gl = 0.f, ge = 0.f, h = 0.f;
+    // scales outside the fast path's range come last: what they meet may be 0, and then the result is
+    const float before = a.careful ? 1.f : a.scale, after = a.careful ? a.scale : 1.f;
     if (a.g_logp) {
         const Id target = ((const Id*)a.targets)[r];
-        gl = a.g_logp[r] * a.scale;
+        gl = a.g_logp[r] * before;
         if (target >= 0 && (int64_t)target < a.V) t = (int)target;
         else gl = 0.f;
         if ((int64_t)target >= a.V && v0 == 0 && threadIdx.x == 0) set_status(a.ws, MOE_ERR_DEVICE_CHECK);
     }
-    if (a.g_entropy) ge = a.g_entropy[r] * a.scale, h = a.entropy[r];
+    if (a.g_entropy) ge = a.g_entropy[r] * before, h = a.entropy[r];
     const bool empty = g.ls == -INFINITY;                            // masked throughout: no gradient
     g.g2 = -ge;
     g.g1 = -fmaf(ge, h, gl);
@@ -932,7 +942,7 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const __gri
             if (j >= j1) continue;
             float d = grad_one(to_f32<T>(x[i]), g);
             if (j == t && to_f32<T>(x[i]) != -INFINITY) d += gl;     // a masked target has no part
-            out[j] = from_f32<T>(empty ? 0.f : d);
+            out[j] = from_f32<T>(empty ? 0.f : d * after);
         }
     }
 }
