@@ -95,3 +95,26 @@ def test_the_example_fits_its_batch():
     from token_dispatch_expert_top_gb300 import lm as L
     losses = L.main(steps=10)
     assert losses[-1] < 0.5 * losses[0]
+
+
+def test_backward_wants_its_own_forward(lm):
+    """The logits are overwritten by backward and by score: gradients of them again, or of a
+    score's, would be of something else."""
+    ids, targets = _tokens(lm, 8)
+    g = torch.ones(128, device="cuda")
+    lm.forward_train(ids, targets)
+    lm.backward(g, weights=False)
+    with pytest.raises(RuntimeError):
+        lm.backward(g, weights=False)
+    lm.forward_train(ids, targets)
+    lm.score(ids, targets)
+    with pytest.raises(RuntimeError):
+        lm.backward(g, weights=False)
+    lm.forward_train(ids, targets)
+    want = [t.clone() for t in (lm.logits, lm.h)]
+    first = lm.backward(g, weights=False)[0].clone()
+    lm.score(ids, targets)
+    lm.step -= 1                                           # the same dropout again
+    lm.forward_train(ids, targets)
+    assert torch.equal(lm.logits, want[0]) and torch.equal(lm.h, want[1])
+    assert torch.equal(lm.backward(g, weights=False)[0], first)

@@ -32,6 +32,7 @@ class MoeLM:
                  seed: int = 0):
         self.layer, self.table = layer, table.contiguous()
         self.embed_scale, self.dropout, self.seed, self.step = embed_scale, dropout, seed, 0
+        self.kept = False                                     # what `backward` needs is in place
         V, H = table.shape
         N, dev = layer.w.N, table.device
         f32 = dict(dtype=torch.float32, device=dev)
@@ -48,7 +49,8 @@ class MoeLM:
     def score(self, ids: torch.Tensor, targets: torch.Tensor, n_top: int = 0, temperature: float = 1.0):
         """(logp, entropy, top_idx, top_logp) of the targets' and the n_top likeliest tokens,
         without dropout; every tensor is the model's own and is overwritten by the next call
-        (the top lists are new)."""
+        (the top lists are new).  What an earlier forward_train kept for `backward` is lost."""
+        self.kept = False
         M.moe_embedding(ids, self.table, self.x0, self.embed_scale, self.ws)
         y = self.layer.forward(self.x0)
         M.moe_dropout(y, self.h, 0.0, self.seed, 0, residual=self.x0)
@@ -63,6 +65,7 @@ class MoeLM:
     def forward_train(self, ids: torch.Tensor, targets: torch.Tensor):
         """(logp, entropy) of the targets, keeping what `backward` needs.  Negative ids and
         targets are padding."""
+        self.kept = False
         self.ids, self.targets = ids, targets
         self.step += 1
         M.moe_embedding(ids, self.table, self.x0, self.embed_scale, self.ws)
@@ -70,11 +73,16 @@ class MoeLM:
         M.moe_dropout(y, self.h, self.dropout, self.seed, self.step, residual=self.x0)
         torch.mm(self.h, self.table.t(), out=self.logits)
         M.moe_token_logprobs(self.logits, targets, self.logp, self.entropy, self.stats, scale=1.0, ws=self.ws)
+        self.kept = True
         return self.logp, self.entropy
 
     def backward(self, g_logp: torch.Tensor, g_entropy: torch.Tensor | None = None, weights: bool = True):
         """Gradients of the last forward_train for the gradients of its two results:
-        (dtable, the layer's (dW_router, dbias, dW_gate_up, dW_down)).  Overwrites the logits."""
+        (dtable, the layer's (dW_router, dbias, dW_gate_up, dW_down)).  Overwrites the logits: once
+        per forward_train, and before any `score`."""
+        if not self.kept:
+            raise RuntimeError("backward: no forward_train's tensors are kept (one backward each, no score between)")
+        self.kept = False
         M.moe_token_logprobs_backward(self.logits, self.targets, self.stats,
                                       None if g_entropy is None else self.entropy, g_logp, g_entropy, self.logits,
                                       1.0, self.ws)
