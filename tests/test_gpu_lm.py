@@ -118,3 +118,21 @@ def test_backward_wants_its_own_forward(lm):
     lm.forward_train(ids, targets)
     assert torch.equal(lm.logits, want[0]) and torch.equal(lm.h, want[1])
     assert torch.equal(lm.backward(g, weights=False)[0], first)
+
+
+def test_the_tables_gradient_keeps_its_32_bits(lm):
+    """The head's part and the embedding's are sums of FP32 precision, not rounded to BF16 between.
+    The head's: products of two BF16 numbers are exact in FP32, and N of them are added, each
+    addition off by at most 2^-23 of the absolute sum (2^-24, or twice that where the tensor
+    cores cut bits off); the embedding's adds a row per token of the id, the scale's rounding and its
+    own addition onto the head's."""
+    ids, targets = _tokens(lm, 9)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    lm.forward_train(ids, targets)
+    h = _f64(lm.h)
+    dtable, _ = lm.backward(torch.randn(128, generator=gen, device="cuda"), weights=False)
+    dl, dx0, i = _f64(lm.logits), _f64(lm.dx0), to_np(ids)
+    emb, emb_abs, count = P.embedding_grad(i, dx0, 301, 16.0)
+    ref, size = dl.T @ h + emb, np.abs(dl).T @ np.abs(h) + emb_abs
+    tol = (128 + 4 + count[:, None]) * 2.0 ** -23 * size
+    assert np.all(np.abs(_f64(dtable) - ref) <= tol)

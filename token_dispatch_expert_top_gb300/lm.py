@@ -88,7 +88,7 @@ class MoeLM:
                                       1.0, self.ws)
         dlogits = self.logits
         torch.mm(dlogits, self.table, out=self.dh)
-        self.dtable.copy_(torch.mm(dlogits.t(), self.h))
+        torch.mm(dlogits.t(), self.h, out_dtype=torch.float32, out=self.dtable)   # not rounded to BF16 on the way
         M.moe_dropout(self.dh, self.dy, self.dropout, self.seed, self.step)
         dx, *rest = self.layer.backward(self.dy, self.x0, weights=weights)
         torch.add(dx, self.dh, out=self.dx0)                  # through the layer and past it
