@@ -93,3 +93,43 @@ def test_dropout_large_and_counters_past_32_bits(M):
     assert np.array_equal(to_np(got) != 0, tail >= 16384)
     M.moe_dropout(x, x, 0.25, 5, 6, None, torch.cuda.current_stream())
     assert torch.equal(x, out)
+
+
+@pytest.mark.parametrize("rows,cols,pad,shift", [(33, 520, 0, 0), (33, 521, 3, 1)])
+@pytest.mark.parametrize("p", [0.3, 0.9])
+def test_forward_and_gradient_keep_the_counters_elements(M, rows, cols, pad, shift, p):
+    """Each against the plain form's bits by itself."""
+    keep = torch.from_numpy(P.dropout_bits(rows, cols, 11, 4) >= round(p * 65536)).cuda()
+    for _ in range(2):                                     # an input, and the gradient of the output
+        x = _view(rows, cols, F32, pad, shift).abs_().add_(0.5)
+        out = torch.empty((rows, cols), device="cuda")
+        M.moe_dropout(x, out, p, 11, 4)
+        assert torch.equal(out != 0, keep)
+
+
+@pytest.mark.parametrize("rows,cols,ld", [(2 ** 32 + 64, 1, 1),             # by columns
+                                          (1, 2 ** 35 + 512, 2 ** 35 + 512),  # one long row
+                                          (2 ** 32 + 64, 8, 16)])           # groups of a padded matrix
+def test_dropout_counters_past_32_bits(M, rows, cols, ld):
+    """Elements on both sides of the counter 2^32, in place, against the generator."""
+    torch.cuda.empty_cache()
+    need = rows * ld * 2
+    if torch.cuda.mem_get_info()[0] < need + (8 << 30):
+        pytest.skip(f"{need >> 30} GB of device memory are not free")
+    x = torch.empty((rows, ld), dtype=BF16, device="cuda")[:, :cols]
+    groups = (cols + 7) // 8
+    width = min(cols, 8)
+    counters = [0, 1, 77, 2 ** 31, 2 ** 32 - 1, *range(2 ** 32, 2 ** 32 + 64)]
+    at = [(x[b // groups, b % groups * 8:b % groups * 8 + width], b) for b in counters]
+    for part, _ in at:
+        part.fill_(1.0)
+    seed, offset, p, m = 0x123456789ABCDEF, 3, 0.5, 0xFFFFFFFF
+    M.moe_dropout(x, x, p, seed, offset)
+    got = torch.stack([part for part, _ in at]).cpu() != 0
+    want = []
+    for b in counters:
+        w = P.philox([b & m, b >> 32, offset, 0], [seed & m, seed >> 32])
+        want.append([(w[i // 2] >> 16 * (i % 2) & 0xFFFF) >= 32768 for i in range(width)])
+    assert torch.equal(got, torch.tensor(want))
+    del x, at, part
+    torch.cuda.empty_cache()

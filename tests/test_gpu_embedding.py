@@ -226,3 +226,43 @@ def test_embedding_grad_in_a_longer_batchs_workspace(M, longest, N, H):
     ref = torch.zeros((V, H), device="cuda").index_add_(0, ids.clamp(min=0), dout * (ids >= 0).unsqueeze(1))
     assert torch.equal(dtable, ref)                        # whole numbers: exact in any order
     assert M.moe_last_device_status(ws) == M.MOE_OK
+
+
+def _many_ids(kind, N, V):
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    n = torch.arange(N, device="cuda")
+    if kind == "zipf":
+        u = torch.rand(N, generator=gen, device="cuda", dtype=torch.float64)
+        return (torch.exp(u * np.log(V + 1.0)).long() - 1).clamp(0, V - 1)
+    if kind == "one":
+        return torch.full_like(n, 5)
+    if kind == "two in turns":                             # owned by the same CTA
+        return torch.where(n % 2 == 0, 3, 5)
+    if kind == "two in blocks":
+        return torch.where(n < N // 2 + 7, 5, 3)
+    return torch.randint(-V // 4, V, (N,), generator=gen, device="cuda")     # a fifth of padding
+
+
+# One sweep of the ordering covers 4096 ids, and a CTA lists 4096 tokens of its own at a time.
+@pytest.mark.parametrize("N", [4096, 4097, 8192, 8193, 20000])
+@pytest.mark.parametrize("kind", ["zipf", "one", "two in turns", "two in blocks", "padded"])
+@pytest.mark.parametrize("idt", [torch.int32, torch.int64])
+@pytest.mark.parametrize("V,H,accumulate", [(600, 264, False), (70_000, 24, True)])
+def test_embedding_grad_of_many_sweeps(M, N, kind, idt, V, H, accumulate):
+    """Sums of whole numbers, which FP32 adds exactly in any order."""
+    ids = _many_ids(kind, N, V)
+    gen = torch.Generator(device="cuda").manual_seed(H)
+    dout = torch.randint(-8, 9, (N, H), device="cuda", generator=gen).float()
+    ref = torch.full((V, H), 3.0 if accumulate else 0.0, device="cuda")
+    ref.index_add_(0, ids.clamp(min=0), dout * (ids >= 0).unsqueeze(1))
+    ws = _ws(M, M.moe_embedding_workspace_bytes(N, V, H))
+    for dtype in (F32, BF16):
+        dtable = torch.full((V, H), 3.0, device="cuda")
+        M.moe_embedding_backward(ids.to(idt), dout.to(dtype), dtable, 1.0, accumulate, ws)
+        assert torch.equal(dtable, ref)
+    assert M.moe_last_device_status(ws) == M.MOE_OK
+
+
+@pytest.mark.parametrize("kind", ["one", "two in turns", "zipf"])
+def test_embedding_grad_of_many_sweeps_in_fractions(M, kind):
+    _grad_case(M, _many_ids(kind, 9001, 300), 300, 40, F32, F32, scale=0.3)
