@@ -530,8 +530,14 @@ int moe_embedding(const void* ids, int id_bytes, int64_t N, const void* table, i
 
 /* Gradient of the embedding table, by tokens sorted by id:
  *   dtable[v] = scale * sum over n with ids[n] = v of dout[n]   (+ dtable[v], accumulate)
- * summed in FP32, in token order within ranges of 4 to 32 sorted tokens (by N and H
- * alone) and in an order set by their number over the ranges.
+ * summed in FP32, one of two ways:
+ *   - N <= 1024, and either `accumulate` or at most 256 MiB in V x H and 64 MiB in N x H
+ *     elements of dtable's type: in an order set by the number of the id's tokens and H;
+ *   - otherwise: in token order within ranges of 4 to 32 tokens of the list sorted by id
+ *     (their length by N and H, where a range begins in an id's tokens by the other ids, too),
+ *     then the ranges' sums in an order set by their number.
+ * The same arguments give the same bits; the same tokens under another V, table type or
+ * `accumulate` may differ by rounding.
  * Without `accumulate` every row of dtable is written, zeros where no token names it;
  * with it only the rows that tokens name are touched.  Negative ids take no part; an id
  * of V or more takes none and records MOE_ERR_DEVICE_CHECK.
@@ -570,8 +576,8 @@ int moe_token_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int6
  *                             - g_entropy * p_j * (logp_j + entropy) )
  *   stats, entropy : moe_token_logprobs's (entropy only with g_entropy)
  *   dlogits : [T][V] (dtype); may be the logits themselves (with ld_dlogits = ld) (out)
- * Masked logits and rows that are masked throughout get 0; a row without a target gets
- * the entropy's part only. */
+ * Masked logits and rows that are masked throughout get 0, a row with a NaN or +inf gets NaN;
+ * a row without a target gets the entropy's part only. */
 int moe_token_logprobs_backward(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
                                 float scale, const void* targets, int id_bytes, const float* stats,
                                 const float* entropy, const float* g_logp, const float* g_entropy,

@@ -86,7 +86,7 @@ struct RawCols {
 
 // A memory-bound copy with a scale.  Short rows (aligned, at most 128 columns): 2^lane_bits
 // lanes per row, each one group of eight columns.  Otherwise one warp per 256 * U columns of
-// a row; its loads are all issued before the first store.  8192 rows of 7168 BF16 in 30.1 us
+// a row; its loads are all issued before the first store.  8192 rows of 7168 BF16 in 29.9 us
 // (7.7 TB/s, some of it L2's); a single row is bound by the launch.
 constexpr int kEmbedUnroll = 4;
 template <typename Id, typename In, typename Out, bool VECTOR>
@@ -461,8 +461,8 @@ static cudaError_t launch_fill_t(const EmbedBackward& c, cudaStream_t stream) {
     const int64_t row_bytes = c.H * (int64_t)sizeof(Grad);
     const int fill_rows = row_bytes > kFillBytes / 2 ? 1 : (int)(kFillBytes / row_bytes);
     const int64_t blocks = (c.V + fill_rows - 1) / fill_rows;
-    return launch_after(embed_fill_kernel<Grad>, blocks, kFillThreads, 0, 1, stream, (const uint32_t*)c.present, c.V, c.H,
-                        (Grad*)c.dtable, c.ld_dtable, fill_rows);
+    return launch_after(embed_fill_kernel<Grad>, blocks, kFillThreads, 0, 1, stream, (const uint32_t*)c.present, c.V,
+                        c.H, (Grad*)c.dtable, c.ld_dtable, fill_rows);
 }
 
 // Lists the run of id k that begins in `range` and goes on: how many partial rows it has (its
@@ -489,8 +489,11 @@ __device__ __forceinline__ void list_crossing(const EmbedSumArgs& a, int range, 
 }
 
 // One warp per (range of places, 256 columns), bound by the latency of the rows' loads, eight
-// (FP32: four) of which a lane has in flight.  16384 tokens of 7168 BF16 columns into FP32: 70 us
+// (FP32: four) of which a lane has in flight.  16384 tokens of 7168 BF16 columns into FP32: 69 us
 // beside 445 us for the zero rows of a 3.7 GB table; ordering takes 12 us and the join 7.5.
+// Accumulating onto that table: 114 us, as the rows' old values are read, and 136 us in all.  The
+// ordering's time grows with N, as every CTA reads all ids (131072 tokens: 114 us, and 154 us if they
+// share one id, which one CTA places), and so does the join's for one id (133 us).
 template <typename In, typename Grad, bool VECTOR>
 __global__ void __launch_bounds__(kSumWarps * 32) embed_segment_kernel(const __grid_constant__ EmbedSumArgs a) {
     grid_dependency_wait();
@@ -614,9 +617,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinCtas) embed_join_kernel(
 // as it has tokens, and nothing is exchanged between CTAs.  In a CTA, 2^bits neighbouring lanes
 // hold a row's groups and the others the run's next rows; their FP32 sums are added in
 // pairs.  The first `zero_ctas` CTAs set the rows that no token names to zero, `zero_rows` each.
-//   777 rows of 1409 FP32 columns into 5003: 9.8 us; with nothing else in the stream to overlap
-// 11.0 against 17.2 by sorting (12.9 with three or five CTAs to an SM); one id for all of 1000 rows of 2048: 9.7 against 19.7.  Every CTA reads all
+//   777 rows of 1409 FP32 columns into 5003: 9.9 us; the odd rows, which move by single elements,
+// cost 1.4 of them (9.0 us against 7.6 for 1408 columns, the same rows again and again).  With
+// nothing else in the stream to overlap 11.0 us against 17.2 by sorting, and 12.9 with three or
+// five CTAs to an SM; one id for all of 1000 rows of 2048: 9.7 against 19.7.  Every CTA reads all
 // ids, so the work grows with N^2: at 2000 tokens it took 27.2 us against 18.8.
+//   Bound by latency: of 17 cycles between a warp's instructions 5 are waits for memory and 39% of
+// the issue slots are taken; the rest is barriers and the chain from ids to rows to stores.
 constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32;
 constexpr int kFewTokens = 1024, kFewSweeps = kFewTokens / kFewThreads;
 constexpr int kFewCols = kFewThreads * 8;
@@ -741,8 +748,7 @@ __global__ void __launch_bounds__(kFewThreads, 4) embed_few_kernel(const __grid_
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum[j] += v[j];
     }
-    if (!alone)
-    for (int half = step / 2; half; half /= 2) {
+    for (int half = alone ? 0 : step / 2; half; half /= 2) {
         if (r >= half && r < 2 * half) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) sums[j][tid] = sum[j];

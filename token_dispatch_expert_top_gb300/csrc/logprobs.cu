@@ -345,8 +345,8 @@ struct LaneSums {
 };
 
 // One cluster of CTAs per row (each takes a contiguous share of the row's chunks), one pass
-// over the row: 8192 x 127901 BF16 in 299 us (7.0 TB/s), with the top 8 in 318 us.  The pass is
-// bound by HBM: 8 copies of 16 bytes per lane are in flight, 32 warps an SM, and per BF16
+// over the row: 8192 x 127901 BF16 in 286 us (7.3 TB/s), with the top 8 in 312 us; 4096 x 128000
+// FP32 in 286 and 304 us.  The pass is bound by HBM: 8 copies of 16 bytes per lane are in flight, 32 warps an SM, and per BF16
 // logit about 7 instructions are issued, one of them the exponential.  With the top list it
 // is the latency of each row's end that shows, which the other rows in flight do not hide.
 // For the top list the pass only keeps the lanes' maxima of one or two chunks (a chunk is what
@@ -356,7 +356,7 @@ struct LaneSums {
 // against a bound that rises, cost 12200 warp instructions a row of 128000; this costs 7100
 // beside the pass's 29100.)  In a cluster the warps write their sums, and the CTAs their lists,
 // into the shared memory of those that want them, so that a row ends with one barrier of the
-// cluster: one row of 128000 FP32, n = 20, takes 9.7 us, 64 of 50001 BF16, n = 5, 8.6.  Masked logits
+// cluster: one row of 128000 FP32, n = 20, takes 8.6 us, 64 of 50001 BF16, n = 5, 8.3.  Masked logits
 // never count; they fill the list's end by index.  Where the logits' order or ties leave too
 // many, a way whose work does not depend on the logits is taken: the n best logits lie in the
 // n best chunks by (maximum, position), as a chunk below those has n chunks before it, each
@@ -365,7 +365,7 @@ struct LaneSums {
 template <typename T, typename Id, bool TOP, bool CLUSTER>
 __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __grid_constant__ LogprobArgs a) {
     // lists; the chunks read ahead; later chunk_max.  (Copies to shared memory that are not aligned
-    // to its lines of 128 bytes fetch their sectors twice: 340 instead of 316 us.)
+    // to its lines of 128 bytes fetch their sectors twice: 340 instead of 326 us.)
     extern __shared__ __align__(128) uint8_t dynamic_smem[];
     __shared__ RowSums warp_sums[kLpMaxWarps * kLpMaxCluster];
     __shared__ CarefulSums warp_careful[kLpMaxWarps], cta_careful;
@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(kLpMaxWarps * 32, 4) logprobs_kernel(const __g
                     float x[VEC];
                     RowView<T>::unpack(row.load(v, -INFINITY), x);
                     float mx = x[0];
-    #pragma unroll
+#pragma unroll
                     for (int e = 1; e < VEC; ++e) mx = fmaxf(mx, x[e]);
                     key = max(order_of(mx), 1u);
                 }
@@ -820,7 +820,7 @@ cudaError_t launch_token_logprobs(const LogprobCall& c, cudaStream_t stream) {
 // d x_j = p_j (g1 + g2 lp_j) + 1[j = t] scale g_logp with g2 = -scale g_entropy and
 // g1 = -scale (g_logp + g_entropy entropy).  dlogits may be the logits' own buffer: a thread
 // reads its elements before it writes them.  The kernel moves each logit in and its
-// gradient out once, HBM-bound: 4096 x 128000 BF16 in 295 us (7.1 TB/s, part of the logits still in
+// gradient out once, HBM-bound: 4096 x 128000 BF16 in 297 us (7.1 TB/s, part of the logits still in
 // L2).  That leaves about 20 instructions per BF16 logit: whole blocks of a row away from its
 // ends and its target take a path without checks (with them it issued 21 and took 365 us).
 struct LogprobGradArgs {
@@ -959,8 +959,8 @@ static cudaError_t launch_grad_t(LogprobGradArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_token_logprobs_backward(const LogprobGradCall& c, cudaStream_t stream) {
     if (c.T == 0) return cudaSuccess;
-    LogprobGradArgs a{c.logits, c.T, (int)c.V, c.ld, c.scale, !fast_scale(c.scale), c.targets, c.stats, c.entropy, c.g_logp, c.g_entropy,
-                      c.dlogits, c.ld_d, 0, c.ws};
+    LogprobGradArgs a{c.logits, c.T, (int)c.V, c.ld, c.scale, !fast_scale(c.scale), c.targets, c.stats,
+                      c.entropy, c.g_logp, c.g_entropy, c.dlogits, c.ld_d, 0, c.ws};
     if (c.dtype == MOE_F32)
         return c.id_bytes == 8 ? launch_grad_t<float, int64_t>(a, stream) : launch_grad_t<float, int32_t>(a, stream);
     return c.id_bytes == 8 ? launch_grad_t<uint16_t, int64_t>(a, stream) : launch_grad_t<uint16_t, int32_t>(a, stream);
