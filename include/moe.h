@@ -692,7 +692,8 @@ int moe_grad_norm(const moe_adamw_tensor_t* tensors, int count, float max_norm, 
  * tensors of a list, t = step, f = grad_scale or 1:
  *   g = f * grad;   m = beta1 m + (1 - beta1) g;   v = beta2 v + (1 - beta2) g^2
  *   param = param (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
- * in FP32 from the new moments before they are rounded; param and copy are rounded to nearest.
+ * in FP32 from the new moments before they are rounded; param and copy are rounded to nearest, param
+ * once (an infinite weight becomes NaN where weight_decay is not 0).
  * 8-bit moments are rounded up or down at random, so that changes far below their step count
  * on average: a block's scale is the smallest power of two that keeps its magnitudes at or
  * below 448, and x / scale goes to the neighbour away from zero if bits / 65536 is at least 1
