@@ -37,5 +37,11 @@ __device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
     return r;
 }
+// Rounded towards zero.
+__device__ __forceinline__ F2 f2_fma_rz(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
 
 }  // namespace moe
