@@ -24,8 +24,8 @@
 namespace moe {
 namespace {
 
-// A row whose squares overflow FP32 is summed again with its elements at this scale; elements up
-// to FP32's largest then square to at most 2^96.
+// A row whose mean square and eps overflow FP32 is summed again with its elements at this scale (and eps at its
+// square); elements up to FP32's largest then square to at most 2^96.
 constexpr float kDown = 0x1p-80f;
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -535,24 +535,29 @@ __global__ void __launch_bounds__(1024)
         get = get + ring.stage == end ? 0 : get + ring.stage;
         float sum = team_sum<KIND>(pair_sum(squares), t, p, part, turn++);
         fetch();
-        float down = 1.f, eps = a.eps;
-        if (__any_sync(0xffffffffu, sum == INFINITY)) {     // the whole team, or other rows of the warp
+        auto mean_square = [&](float sum, float eps) {
+            return fmaf(sum, inv_cols, fmaf(fminf(sum, FLT_MAX), inv_rest, eps));
+        };
+        float mean = mean_square(sum, a.eps), down = 1.f;
+        if (__any_sync(0xffffffffu, mean == INFINITY)) {    // the whole team, or other rows of the warp
             const F2 by = f2(kDown, kDown);
             squares = f2(0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < P; ++k)
 #pragma unroll
                 for (int i = 0; i < H; ++i) squares = f2_fma(f2_mul(v[k][i], by), f2_mul(v[k][i], by), squares);
-            const float again = team_sum<KIND>(pair_sum(squares), t, p, part, turn++);
-            if (sum == INFINITY) {
-                down = kDown, eps = 0.f, sum = again;
+            sum = team_sum<KIND>(pair_sum(squares), t, p, part, turn++);
+            if (mean == INFINITY) {
+                down = inv_root(mean_square(sum, a.eps * kDown * kDown));
+                // at most 2^92 with an element; in one factor a subnormal number
 #pragma unroll
                 for (int k = 0; k < P; ++k)
 #pragma unroll
-                    for (int i = 0; i < H; ++i) v[k][i] = f2_mul(v[k][i], by);
+                    for (int i = 0; i < H; ++i) v[k][i] = f2_mul(f2_mul(v[k][i], f2(down, down)), by);
+                down *= kDown, mean = 1.f;
             }
         }
-        const float rstd = inv_root(fmaf(sum, inv_cols, fmaf(fminf(sum, FLT_MAX), inv_rest, eps)));
+        const float rstd = inv_root(mean);
         if (keeper && live) a.rstd[r] = rstd * down;
         const F2 by = f2(rstd, rstd);
 #pragma unroll
@@ -606,20 +611,24 @@ __global__ void __launch_bounds__(WARP_ROW ? 128 : CHUNKS == 4 ? 512 : 1024)
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum = fmaf(v[j][i], v[j][i], sum);
     sum = row_sum<WARP_ROW>(sum, part[0]);
-    float down = 1.f, eps = a.eps;
-    if (isinf(sum)) {
-        down = kDown, eps = 0.f, sum = 0.f;
+    float down = 1.f, mean = sum / (float)a.cols + a.eps;
+    if (isinf(mean)) {
+        down = kDown, sum = 0.f;
 #pragma unroll
         for (int j = 0; j < CHUNKS; ++j)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                v[j][i] *= kDown;
-                sum = fmaf(v[j][i], v[j][i], sum);
-            }
-        sum = row_sum<WARP_ROW>(sum, part[1]);
+            for (int i = 0; i < 8; ++i) sum = fmaf(v[j][i] * kDown, v[j][i] * kDown, sum);
+        mean = row_sum<WARP_ROW>(sum, part[1]) / (float)a.cols + a.eps * kDown * kDown;
     }
-    const float rstd = inv_root(sum / (float)a.cols + eps);
+    float rstd = inv_root(mean);
     if (a.rstd && warp == 0 && lane == 0) a.rstd[r] = rstd * down;
+    if (down != 1.f) {                                      // one after the other, as above
+#pragma unroll
+        for (int j = 0; j < CHUNKS; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[j][i] = v[j][i] * rstd * kDown;
+        rstd = 1.f;
+    }
 #pragma unroll
     for (int j = 0; j < CHUNKS; ++j) {
         const int64_t c0 = (int64_t)(j * warps + warp) * 256;
@@ -666,25 +675,25 @@ __global__ void __launch_bounds__(1024) rms_norm_long_kernel(const __grid_consta
         sum += t;
     }
     sum = row_sum<false>(sum, part[0]);
-    float down = 1.f, eps = a.eps;
-    if (isinf(sum)) {
-        down = kDown, eps = 0.f, sum = 0.f;
+    float down = 1.f, mean = sum / (float)a.cols + a.eps;
+    if (isinf(mean)) {
+        down = kDown, sum = 0.f;
         for (int64_t c0 = warp * 256; c0 < a.cols; c0 += 32 * 256) {
             float v[8];
             load_chunk<T, VEC>(s, c0, a.cols, lane, v);
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum = fmaf(v[i] * kDown, v[i] * kDown, sum);
         }
-        sum = row_sum<false>(sum, part[1]);
+        mean = row_sum<false>(sum, part[1]) / (float)a.cols + a.eps * kDown * kDown;
     }
-    const float rstd = inv_root(sum / (float)a.cols + eps);
+    const float rstd = inv_root(mean);
     if (a.rstd && threadIdx.x == 0) a.rstd[r] = rstd * down;
     for (int64_t c0 = warp * 256; c0 < a.cols; c0 += 32 * 256) {
         float v[8], w[8];
         load_chunk<T, VEC>(s, c0, a.cols, lane, v);
         load_weight<VEC>(a.weight, a.w_dtype, c0, a.cols, lane, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] * down * rstd * w[i];
+        for (int i = 0; i < 8; ++i) v[i] = v[i] * rstd * down * w[i];
         if (a.out_dtype == MOE_F32) {
             if (a.out) store_chunk<float, VEC>((float*)a.out + r * a.ld_out, c0, a.cols, lane, v);
         } else {
