@@ -127,3 +127,14 @@ def test_python_entry_points_refuse_what_they_cannot_pass_on():
         M.AdamWTensors([x, x], [x], [x], [x])
     with pytest.raises(TypeError):
         M.AdamWTensors.of_grads([x.half()])
+
+
+def test_gradients_in_written_memory_are_found():
+    written = [(100, 200, "params[0]"), (200, 300, "m[0]"), (1000, 1004, "v[0]")]
+    for grads, want in (([], None), ([(0, 100), (300, 700), (1004, 8)], None), ([(150, 0)], None),
+                        ([(0, 101)], "grads[0] and params[0]"), ([(199, 1)], "grads[0] and params[0]"),
+                        ([(200, 4)], "grads[0] and m[0]"), ([(0, 50), (120, 4)], "grads[1] and params[0]"),
+                        ([(0, 2000)], "grads[0] and v[0]"), ([(299, 2)], "grads[0] and m[0]"),
+                        ([(900, 100), (1003, 1)], "grads[1] and v[0]")):
+        assert M._first_overlap(written, grads) == want
+    assert M._first_overlap([], [(0, 10)]) is None

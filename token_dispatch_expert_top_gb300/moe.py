@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from bisect import bisect_left
 
 import torch
 
@@ -622,6 +623,17 @@ def moe_rms_norm_backward(dout, s, weight, rstd, dx, dweight=None, dsum=None, ac
         raise MoeError(fn, rc)
 
 
+def _first_overlap(written: list, grads: list) -> str | None:
+    """The first gradient (begin, bytes) that lies in one of the written ranges (begin, end, name), which are in
+    order and apart, and the range's name."""
+    begins = [begin for begin, _, _ in written]
+    for i, (begin, size) in enumerate(grads):
+        k = bisect_left(begins, begin + size) - 1             # the last one that begins before its end
+        if size and k >= 0 and written[k][1] > begin:
+            return f"grads[{i}] and {written[k][2]}"
+    return None
+
+
 class AdamWTensors:
     """The list of tensors that moe_adamw steps and moe_grad_norm measures, checked once and kept
     by a program beside its tensors (it holds on to them).
@@ -630,7 +642,8 @@ class AdamWTensors:
     elements place by place; params and grads FP32 or BF16.  m and v are FP32, or uint8 with
     m_scales and v_scales (lists of uint8, one per 32 elements; None at the places of FP32 moments)
     for moments in MXFP8.  copies: BF16 tensors, or None, which get each new weight.  weight_decay:
-    one number, or one per tensor.  All but the gradients are written, and must not overlap."""
+    one number, or one per tensor.  All but the gradients are written, and must not overlap; nor may a
+    gradient lie in memory that is written, for moe_adamw (gradients may overlap each other)."""
 
     def __init__(self, params, grads, m, v, copies=None, m_scales=None, v_scales=None, weight_decay=0.0):
         fn, k = "AdamWTensors", len(params)
@@ -659,10 +672,10 @@ class AdamWTensors:
             if copy is not None:
                 e.copy = self._vector(f"copies[{i}]", copy, torch.bfloat16, n)
             e.weight_decay = wd
-        written = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), f"{name}[{i}]")
-                         for name, x in lists.items() if name not in ("grads", "weight_decay")
-                         for i, t in enumerate(x) if t is not None and t.numel())
-        for (_, end, one), (begin, _, two) in zip(written, written[1:]):
+        self._written = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), f"{name}[{i}]")
+                               for name, x in lists.items() if name not in ("grads", "weight_decay")
+                               for i, t in enumerate(x) if t is not None and t.numel())
+        for (_, end, one), (begin, _, two) in zip(self._written, self._written[1:]):
             if begin < end:
                 raise ValueError(f"{fn}: {one} and {two} overlap; memory that a step writes must not be there twice")
         self.set_grads(grads)
@@ -671,6 +684,7 @@ class AdamWTensors:
     def of_grads(cls, grads) -> "AdamWTensors":
         """A list of gradients alone, for moe_grad_norm."""
         self = cls.__new__(cls)
+        self._written = []
         self._start([g.numel() for g in grads])
         self.set_grads(grads)
         return self
@@ -702,6 +716,7 @@ class AdamWTensors:
         for e, (pointer, dtype) in zip(self.entries, found):
             e.grad, e.grad_dtype = pointer, dtype
         self._grads = list(grads)
+        self._clash = _first_overlap(self._written, [(g.data_ptr(), g.numel() * g.element_size()) for g in grads])
 
 
 def _list_device(fn: str, tensors: AdamWTensors) -> int:
@@ -741,6 +756,8 @@ def moe_adamw(tensors: AdamWTensors, lr, step, beta1: float = 0.9, beta2: float 
     if not 0 <= seed < 1 << 64:
         raise ValueError(f"{fn}: seed is an unsigned 64-bit number")
     device = _list_device(fn, tensors)
+    if tensors._clash:
+        raise ValueError(f"{fn}: {tensors._clash} overlap; a step must not write over the gradients it reads")
     lr_at, step_at, scale_at = None, None, None
     if isinstance(lr, torch.Tensor):
         lr, lr_at = 0.0, _at(fn, "lr", lr, torch.float32, 1, device)
