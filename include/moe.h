@@ -700,7 +700,9 @@ int moe_grad_norm(const moe_adamw_tensor_t* tensors, int count, float max_norm, 
  * minus its distance from the neighbour towards zero (as a share of their distance).  Element i
  * of tensor number k of the list takes the 16 bits number i % 8 (low half of the first word first)
  * of Philox4x32-10 with key (seed low, seed high) and counter (i / 8 low, i / 8 high, step low
- * word, k) for m, and those of element i ^ 1 for v.  A positive sqrt(v) is never rounded to 0.
+ * word, k) for m, and those of element i ^ 1 for v.  (moe_dropout's counters are (column group, offset):
+ * the two take the same bits for the same seed; give them different ones.)  A positive sqrt(v) is never
+ * rounded to 0.
  * A gradient that is not finite, or whose square is not, spoils its element's moments and weight (with
  * an infinity, the 8-bit moments of its block of 32): grad_scale keeps such a step out.
  * Squares below FP32's normal numbers (gradients below about 1e-19) count as zero or nearly so.

@@ -131,6 +131,27 @@ def test_optimiser_keeps_out_a_step_that_is_not_finite():
     assert not torch.equal(before[1], lm.table)
 
 
+def test_dropout_and_the_rounding_of_moments_take_different_bits():
+    """Both default to one seed, and count steps from 1 and element groups from 0."""
+    from token_dispatch_expert_top_gb300.lm import LmOptimizer
+    lm, ids, targets = _model()
+    lm.seed = 0
+    opt = LmOptimizer(lm, eight_bits=True)
+    lm.forward_train(ids, targets)
+    lm.backward(torch.ones(128, device="cuda") / 128, weights=False)
+    opt.step()
+    n = 8192
+    e = opt.tensors.entries[0]
+    m, _ = T.moments(_f64(lm.dtable).reshape(-1)[:n], 0.0, 0.0, 0.9, 0.95, float(opt.factor))
+    codes, scales = (t.reshape(-1).cpu().numpy().astype(np.int64) for t in opt.tensors._kept[1][:1] + opt.tensors._kept[4][:1])
+    assert e.m == opt.tensors._kept[1][0].data_ptr()
+
+    def agreeing(seed):
+        return (T.encode(m, scales[:n // 32], T.bits16(n, seed, 1, 0), False) == codes[:n]).mean()
+
+    assert agreeing(opt.seed) >= 0.999 and agreeing(lm.seed) <= 0.9
+
+
 def test_a_captured_step_is_the_step():
     """Forward, backward and update replayed from one graph, against the same steps called directly."""
     from token_dispatch_expert_top_gb300.lm import LmOptimizer

@@ -147,11 +147,14 @@ class LmOptimizer:
     The table has FP32 master weights, whose BF16 copy is the model's table; the norms' weights and
     the router's are stepped in place.  (The layer holds its expert weights packed for its GEMMs; their
     gradients are the caller's.)  eight_bits: moments of the matrices in MXFP8 codes, a quarter of their
-    memory.  The step number is on the device, so that a step can be captured."""
+    memory; seed: of their rounding, whose bits are others than those of a dropout of the same seed.  The step
+    number is on the device, so that a step can be captured."""
+
+    DOMAIN = int.from_bytes(b"moe_adam", "big")               # both draw from the same counters: another key
 
     def __init__(self, lm: MoeLM, lr: float = 1e-3, betas=(0.9, 0.95), eps: float = 1e-8, weight_decay: float = 0.1,
                  max_norm: float = 1.0, eight_bits: bool = False, seed: int = 0):
-        self.lm, self.betas, self.eps, self.max_norm, self.seed = lm, betas, eps, max_norm, seed
+        self.lm, self.betas, self.eps, self.max_norm, self.seed = lm, betas, eps, max_norm, seed ^ self.DOMAIN
         dev = lm.table.device
         self.master = lm.table.float()
         params, copies = [self.master, lm.layer.w_router], [lm.table, None]
