@@ -131,6 +131,25 @@ def test_optimiser_keeps_out_a_step_that_is_not_finite():
     assert not torch.equal(before[1], lm.table)
 
 
+def test_steps_below_the_routers_last_place_add_up():
+    """64 steps of 1e-5, where half a last place of the router's BF16 weights is 1e-4.  FP32 weights and moments
+    round each step: 64 times 3 u of the weight and 2^-16 of the step; then half a step of BF16."""
+    from token_dispatch_expert_top_gb300.lm import LmOptimizer
+    lm, ids, targets = _model()
+    opt = LmOptimizer(lm, lr=1e-5, max_norm=float("inf"))
+    lm.forward_train(ids, targets)
+    lm.backward(torch.ones(128, device="cuda"), weights=False)
+    p = start = _f64(lm.layer.w_router)
+    g, m, v = _f64(lm.layer.dw_router), 0.0, 0.0
+    for t in range(1, 65):
+        opt.step()
+        m, v = T.moments(g, m, v, 0.9, 0.95)
+        p, _ = T.update(p, m, v, float(np.float32(1e-5)), 0.9, 0.95, 1e-8, 0.0, t)
+    tol = 64 * (3 * U * (np.abs(start) + 1e-3) + 1e-5 * 2.0 ** -16) + 2.0 ** -8 * np.abs(p)
+    assert np.all(np.abs(_f64(lm.layer.w_router) - p) <= tol * (1 + 2.0 ** -8))
+    assert (np.abs(p - start) > 2 * tol).mean() > 0.5          # a router left as it was is out of that
+
+
 def test_dropout_and_the_rounding_of_moments_take_different_bits():
     """Both default to one seed, and count steps from 1 and element groups from 0."""
     from token_dispatch_expert_top_gb300.lm import LmOptimizer

@@ -144,8 +144,8 @@ class MoeLM:
 class LmOptimizer:
     """AdamW over a MoeLM's table, norm weights and router, with the gradients' global norm clipped.
 
-    The table has FP32 master weights, whose BF16 copy is the model's table; the norms' weights and
-    the router's are stepped in place.  (The layer holds its expert weights packed for its GEMMs; their
+    The table and the router have FP32 master weights, whose BF16 copies are the model's (a step below half a
+    last place of BF16 would be lost otherwise); the norms' weights are stepped in place.  (The layer holds its expert weights packed for its GEMMs; their
     gradients are the caller's.)  eight_bits: moments of the matrices in MXFP8 codes, a quarter of their
     memory; seed: of their rounding, whose bits are others than those of a dropout of the same seed.  The step
     number is on the device, so that a step can be captured."""
@@ -156,8 +156,8 @@ class LmOptimizer:
                  max_norm: float = 1.0, eight_bits: bool = False, seed: int = 0):
         self.lm, self.betas, self.eps, self.max_norm, self.seed = lm, betas, eps, max_norm, seed ^ self.DOMAIN
         dev = lm.table.device
-        self.master = lm.table.float()
-        params, copies = [self.master, lm.layer.w_router], [lm.table, None]
+        self.master, self.router_master = lm.table.float(), lm.layer.w_router.float()
+        params, copies = [self.master, self.router_master], [lm.table, lm.layer.w_router]
         grads, decay = [lm.dtable, lm.layer.dw_router], [weight_decay, 0.0]
         if lm.norm_eps is not None:
             params += [lm.w_in, lm.w_out]
