@@ -683,7 +683,8 @@ typedef struct {
  *   max_norm : positive (infinity: factor is 1)
  *   workspace : moe_grad_norm_workspace_bytes() bytes
  * Squares and their sums are FP32 (a norm beyond 2^63 is infinite, a gradient below 2^-75 counts as
- * zero), added in an order set by the list's sizes. */
+ * zero), added in an order set by the list's sizes and types and by where in 16 bytes each gradient begins: the
+ * same bits for the same gradients wherever they lie otherwise. */
 size_t moe_grad_norm_workspace_bytes(void);
 int moe_grad_norm(const moe_adamw_tensor_t* tensors, int count, float max_norm, float* norm, float* factor,
                   void* workspace, size_t workspace_bytes, void* stream);
