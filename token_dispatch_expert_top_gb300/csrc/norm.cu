@@ -1163,7 +1163,8 @@ __global__ void __launch_bounds__(1024)
 }
 
 // Rows that the ring does not take and registers do not hold: the row is read twice by its block, and the
-// weight gradient is summed by a kernel of its own.  4096 x 16384 BF16 with dsum 299 us (1.8 TB/s).
+// weight gradient is summed by a kernel of its own.  4096 x 16385 BF16 with dsum 266 us, 8000 x 8193 301 (single-element
+// accesses, three passes); aligned, 1024 x 65544 198 us (2.7 TB/s).
 template <typename T, typename TG, bool VEC>
 __global__ void __launch_bounds__(1024) rms_norm_grad_long_kernel(const __grid_constant__ RmsNormGradCall a) {
     __shared__ float part[32];
@@ -1309,6 +1310,15 @@ bool launch_grad_ring(const RmsNormGradCall& c, cudaStream_t stream, int64_t& pa
     return true;
 }
 
+// Shares of the rows for rms_norm_dw_long_kernel: 32 rows one after another, as far as kNormParts shares allow
+// (in 16 shares whatever the rows, FP32 sums were 8192 additions deep at 131072 of them, and too few blocks read:
+// 8000 x 8193 BF16 with dsum 761 us, 301 so).
+int64_t long_parts(int64_t rows) {
+    int64_t parts = (rows + 31) / 32;
+    if (parts < 16) parts = rows < 16 ? rows : 16;
+    return parts < kNormParts ? parts : kNormParts;
+}
+
 template <typename T, typename TG>
 cudaError_t launch_grad_rows(const RmsNormGradCall& c, bool vec, cudaStream_t stream) {
     const int64_t chunks = (c.cols + 255) / 256;
@@ -1333,7 +1343,7 @@ cudaError_t launch_grad_rows(const RmsNormGradCall& c, bool vec, cudaStream_t st
                      : launch_after(rms_norm_grad_kernel<T, TG, 2, false>, parts, threads, 0, 1, stream, c);
     } else if (c.rows > 0) {
         if (c.dweight) {
-            parts = c.rows < 16 ? c.rows : 16;
+            parts = long_parts(c.rows);
             const int64_t blocks = (chunks + 3) / 4;
             auto go = [&](auto k) { e = launch_after(k, parts * blocks, 128, 0, 1, stream, c, (int)parts, blocks); };
             vec ? go(rms_norm_dw_long_kernel<T, TG, true>) : go(rms_norm_dw_long_kernel<T, TG, false>);
