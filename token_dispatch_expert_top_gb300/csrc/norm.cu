@@ -1226,7 +1226,8 @@ __global__ void __launch_bounds__(128) rms_norm_dw_long_kernel(const __grid_cons
 }
 
 // dweight (+)= the sum of `rows` partial rows, in the same order every time: warp k adds rows k, k + 32, ...,
-// then the warps' sums are added in order.
+// then the warps' sums are added in pairs (one after another they are 32 roundings deep: 777 x 1409 FP32 was 1.31e-7 off
+// 64-bit arithmetic, so it is 1.00e-7, as a plain FP32 sum).
 __global__ void __launch_bounds__(1024) rms_norm_dw_join_kernel(const float* part, int64_t rows, int64_t cols,
                                                                 float* dweight, int accumulate) {
     __shared__ float sums[32][33];
@@ -1239,10 +1240,14 @@ __global__ void __launch_bounds__(1024) rms_norm_dw_join_kernel(const float* par
     sums[warp][lane] = t;
     __syncthreads();
     if (warp == 0 && c < cols) {
-        t = 0.f;
+        float v[32];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) t += sums[k][lane];
-        dweight[c] = accumulate ? dweight[c] + t : t;
+        for (int k = 0; k < 32; ++k) v[k] = sums[k][lane];
+#pragma unroll
+        for (int n = 16; n; n /= 2)
+#pragma unroll
+            for (int k = 0; k < n; ++k) v[k] += v[k + n];
+        dweight[c] = accumulate ? dweight[c] + v[0] : v[0];
     }
 }
 
