@@ -690,7 +690,7 @@ class AdamWTensors:
         return self
 
     def _start(self, sizes):
-        self.count, self.device = len(sizes), None
+        self.count, self.device, self._sizes = len(sizes), None, sizes
         self.entries = (AdamWTensor * max(1, self.count))()
         for e, n in zip(self.entries, sizes):
             e.n = n
@@ -712,11 +712,12 @@ class AdamWTensors:
         """Other tensors for the gradients, of the same sizes."""
         if len(grads) != self.count:
             raise ValueError(f"AdamWTensors: grads has {len(grads)} entries, not {self.count}")
-        found = [self._float(f"grads[{i}]", g, e.n) for i, (e, g) in enumerate(zip(self.entries, grads))]
+        found = [self._float(f"grads[{i}]", g, n) for i, (n, g) in enumerate(zip(self._sizes, grads))]
         for e, (pointer, dtype) in zip(self.entries, found):
             e.grad, e.grad_dtype = pointer, dtype
         self._grads = list(grads)
-        self._clash = _first_overlap(self._written, [(g.data_ptr(), g.numel() * g.element_size()) for g in grads])
+        self._clash = _first_overlap(self._written, [(pointer, 4 * n if dtype == MOE_F32 else 2 * n)
+                                                      for (pointer, dtype), n in zip(found, self._sizes)])
 
 
 def _list_device(fn: str, tensors: AdamWTensors) -> int:
