@@ -201,7 +201,7 @@ inline Kind kind_of(const moe_adamw_tensor_t& t) {
 constexpr int kStepThreads = 256, kEightThreads = 128;
 // Moments in 8 bits: neighbouring blocks take the groups of a stretch in turn, so that what is read and written
 // at a time lies together (352M BF16 weights, 32 groups to a block: 664 us where each has groups of its
-// own in a row, 575 in turns of 4 to 256).
+// own in a row, 577 in turns of 4 to 256).
 constexpr int kTurns = 16;
 template <Kind KIND>
 constexpr int kThreads = KIND == kF32Moments ? kStepThreads : kEightThreads;
@@ -685,7 +685,7 @@ cudaError_t launch_adamw_list(const moe_adamw_tensor_t* t, int first, int count,
     a.number0 = (uint32_t)first, a.s = s, a.groups = 1;
     if (KIND != kF32Moments) {
         // several groups to a block spread its search and scalars, where that leaves enough blocks (352M BF16
-        // weights: 584 us with eight, 575 with 32)
+        // weights: 2% more with eight)
         int64_t all = 0;
         for (int i = 0; i < count; ++i) all += kind_of(t[first + i]) == KIND ? t[first + i].n / kGroup : 0;
         if (all >= (int64_t)num_sms * 64) a.groups = 8;

@@ -11,8 +11,9 @@
 //   4096 x 16384 BF16, residual             108 us (5.0 TB/s)      gradient, 4096 x 16384 BF16, dsum  145 us (3.7 TB/s)
 //
 // Three ways, by the rows: through shared memory (below: up to 8192 columns, up to 65536 where rows are
-// aligned); rows whose matrices begin at different elements of eight, in registers; all others, read twice.  The
-// latter two deal a row in chunks of 256 columns per warp: aligned, lane l has columns 8l .. 8l+7; otherwise
+// aligned); in registers, up to 8192 or 16384 columns, what the first does not take (matrices other than BF16 whose
+// rows begin at different elements of eight, few rows that begin anywhere, MXFP8 copies of such rows); all others, read
+// twice.  The latter two deal a row in chunks of 256 columns per warp: aligned, lane l has columns 8l .. 8l+7; otherwise
 // columns l, l+32, ..., so that the lanes touch neighbouring elements.  Always a block of 32 columns (one MXFP8
 // scale) lies within a warp.
 #include <float.h>
@@ -149,8 +150,8 @@ __device__ __forceinline__ void round_to(float (&v)[8]) {
 // last piece are masked.  A thread's rows are a multiple of E apart, so that its shift is the same for
 // all of them and its weights and sums stay in registers.
 // SHIFTED: BF16 rows that begin so in what is written, and anywhere else in what is read: a thread copies the two
-// aligned pieces that hold its own, and shifts it out of them (8091 x 7168 in rows of 7169: 67 us, by single elements
-// 100; gradient with dsum 186, 230; 139423 x 416 71 and 87, gradient 180 and 282.  Words of four bytes, one more than
+// aligned pieces that hold its own, and shifts it out of them (8091 x 7168 in rows of 7169: 65 us, by single elements
+// 100; gradient with dsum 186, 230; 139423 x 416 66 and 87, gradient 181 and 282.  Words of four bytes, one more than
 // the piece has, in place of the second piece: 68 and 198, 74 and 185).
 // WIDE: aligned rows of more columns, by a cluster of two to eight blocks, `share` columns each, which write
 // their sums into each other's shared memory; bound by the cluster's barrier (read twice by one block, which
@@ -577,7 +578,7 @@ __global__ void __launch_bounds__(1024)
 // Rows of other types than BF16 whose matrices begin at different elements, few rows that begin anywhere, and MXFP8
 // copies of rows that are not aligned: one row by one warp (WARP_ROW, four rows to a block) or by a block, its
 // elements in registers, up to CHUNKS chunks per warp.  Bound by the instructions of single-element accesses: 4045 x
-// 7168 FP32 in rows of 7169 48 us (aligned 39), BF16 of twice as many rows 100 (67 through shared memory).
+// 7168 FP32 in rows of 7169 48 us (aligned 39), BF16 of twice as many rows 100 (65 through shared memory).
 template <typename T, int CHUNKS, bool WARP_ROW>
 __global__ void __launch_bounds__(WARP_ROW ? 128 : CHUNKS == 4 ? 512 : 1024)
     rms_norm_kernel(const __grid_constant__ RmsNormCall a) {
@@ -649,7 +650,8 @@ __global__ void __launch_bounds__(WARP_ROW ? 128 : CHUNKS == 4 ? 512 : 1024)
 }
 
 // Rows of any length, by a block of 1024 threads: the row is read twice, the second time what the
-// first pass left (the sum, or x), mostly in L2 by then.  1024 x 65536 BF16 with a residual 147 us (3.7 TB/s).
+// first pass left (the sum, or x), mostly in L2 by then.  1024 x 65544 BF16 with a residual 151 us
+// (3.6 TB/s), 4096 x 16385 185 (2.9 TB/s; single-element accesses).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(1024) rms_norm_long_kernel(const __grid_constant__ RmsNormCall a) {
     __shared__ float part[2][32];
@@ -793,8 +795,9 @@ struct RowCheck {
 };
 
 // So few rows that begin anywhere are quicker in registers, a block to each: 400 x 1409 BF16 2.6 us (2.9 through
-// shared memory), 777 rows 4.5 (4.1); FP32 1600 x 1409 5.4 (5.7), 3200 rows 9.2 (8.5); gradients 5.9 (6.5), 7.0 (8.8),
-// 9.7 (11.9), 19.9 (17.2).
+// shared memory), 777 rows 4.5 (4.1); FP32 1600 x 1409 5.4 (5.7), 3200 rows 9.2 (8.5).  The gradient goes by the same
+// rule, which is too low for it: 400 rows 5.9 us (6.5), 777 rows, which go through shared memory, 7.0 (8.8); FP32 1600 rows
+// 9.7 (11.9), 3200 rows 19.9 (17.2).
 template <int E>
 bool few_rows(int64_t rows, int64_t cols) {
     return rows * cols < (E == 8 ? 1 << 20 : 5 << 19);
