@@ -145,10 +145,11 @@ class LmOptimizer:
     """AdamW over a MoeLM's table, norm weights and router, with the gradients' global norm clipped.
 
     The table and the router have FP32 master weights, whose BF16 copies are the model's (a step below half a
-    last place of BF16 would be lost otherwise); the norms' weights are stepped in place.  (The layer holds its expert weights packed for its GEMMs; their
-    gradients are the caller's.)  eight_bits: moments of the matrices in MXFP8 codes, a quarter of their
-    memory; seed: of their rounding, whose bits are others than those of a dropout of the same seed.  The step
-    number is on the device, so that a step can be captured."""
+    last place of BF16 would be lost otherwise).  They are taken from the model when this is made: weights loaded
+    into it later want a new optimiser.  The norms' weights are stepped in place.  (The layer holds its expert
+    weights packed for its GEMMs; their gradients are the caller's.)  eight_bits: moments of the matrices in MXFP8
+    codes, a quarter of their memory; seed: of their rounding, whose bits are others than those of a dropout of the
+    same seed.  The step number is on the device, so that a step can be captured."""
 
     DOMAIN = int.from_bytes(b"moe_adam", "big")               # both draw from the same counters: another key
 
