@@ -796,8 +796,8 @@ struct RowCheck {
 
 // So few rows that begin anywhere are quicker in registers, a block to each: 400 x 1409 BF16 2.6 us (2.9 through
 // shared memory), 777 rows 4.5 (4.1); FP32 1600 x 1409 5.4 (5.7), 3200 rows 9.2 (8.5).  The gradient goes by the same
-// rule, which is too low for it: 400 rows 5.9 us (6.5), 777 rows, which go through shared memory, 7.0 (8.8); FP32 1600 rows
-// 9.7 (11.9), 3200 rows 19.9 (17.2).
+// rule, which is too low for it: 400 rows 5.9 us (6.5), 777 rows, which go through shared memory, 7.0 (8.8); FP32
+// 1600 rows 9.7 (11.9), 3200 rows 19.9 (17.2).
 template <int E>
 bool few_rows(int64_t rows, int64_t cols) {
     return rows * cols < (E == 8 ? 1 << 20 : 5 << 19);
